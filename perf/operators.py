@@ -360,7 +360,8 @@ def run(s):
                       blk=s["blk"], page_table=s["table"])
         return s["kw"], s["vw"], s["kc"], s["vc"], s["sc"], st
     if op == "read":
-        return hca.read_quant(s["kc"], s["vc"], s["sc"], s["counts"], s["n"], page_table=s["table"], kc=s["k_out"], vc=s["v_out"])
+        return hca.read_quant(s["kc"], s["vc"], s["sc"], s["counts"], s["n"], page_table=s["table"], k_out=s["k_out"],
+                              v_out=s["v_out"])
     if op == "decode":
         return hca.decode_quant(s["q"], s["kc"], s["vc"], s["sc"], s["kw"], s["vw"], s["seqlens"], s["blk"], s["W"], s["scale"],
                              page_table=s["table"], gq=s["gq"], gk=s["gk"], eps=EPS, gate=s["gates"],
