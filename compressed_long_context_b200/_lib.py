@@ -27,7 +27,8 @@ EXPORTS = ("hca_compress", "hca_prefill", "hca_decode_workspace_size", "hca_deco
            "hca_debug_set_wait_limit", "hca_debug_set_drop_slab", "hca_debug_wait_probe", "hca_gate_logits",
            "hca_prefill_backward_workspace_size", "hca_prefill_backward", "hca_debug_set_backward_segment",
            "hca_debug_set_dsa_rows_limit",
-           "hca_dsa_index", "hca_dsa_topk", "hca_dsa_attend")
+           "hca_dsa_index", "hca_dsa_topk", "hca_dsa_attend",
+           "hca_compress_quant", "hca_append_quant", "hca_read_quant", "hca_decode_quant")
 
 _lib = None
 
@@ -84,6 +85,15 @@ def load():
     lib.hca_dsa_topk.argtypes = [_vp] * 3 + [_i] * 3 + [_vp]
     lib.hca_dsa_attend.restype = _i
     lib.hca_dsa_attend.argtypes = [_vp] * 6 + [_i] * 5 + [_f, _vp]
+    lib.hca_compress_quant.restype = _i
+    lib.hca_compress_quant.argtypes = [_vp] * 6 + [_i] * 6 + [_vp]
+    lib.hca_append_quant.restype = _i
+    lib.hca_append_quant.argtypes = [_vp] * 10 + [_i] * 3 + [_vp] + [_i] * 7 + [_u, _vp]
+    lib.hca_read_quant.restype = _i
+    lib.hca_read_quant.argtypes = [_vp] * 4 + [_i] * 3 + [_vp] * 3 + [_i] * 6 + [_u, _vp]
+    lib.hca_decode_quant.restype = _i
+    lib.hca_decode_quant.argtypes = ([_vp] * 5 + [_i] * 3 + [_vp] * 5 + [_f] + [_vp] * 3 + [_i, _vp, _vp, _sz] + [_i] * 8
+                                     + [_f, _u, _vp])
     lib.hca_debug_set_backward_segment.restype = _i
     lib.hca_debug_set_backward_segment.argtypes = [_i]
     lib.hca_debug_set_dsa_rows_limit.restype = _i

@@ -12,10 +12,13 @@
 #include "common.cuh"
 #include "compress.cuh"
 #include "decode.cuh"
+#include "decode_quant.cuh"
 #include "dsa.cuh"
 #include "gate.cuh"
+#include "merge.cuh"
 #include "prefill.cuh"
 #include "prefill_pair.cuh"
+#include "quant.cuh"
 #include "vha.cuh"
 
 namespace {
@@ -64,6 +67,21 @@ bool make_tmap_4d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, ui
     return r == CUDA_SUCCESS;
 }
 
+// 4-D map over 8-bit codes, box {128, b1, b2, b3}, 128-byte swizzle; strides in bytes for dims 1..3.
+bool make_tmap_4d_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
+                     uint64_t s1, uint64_t s2, uint64_t s3, uint32_t b1, uint32_t b2, uint32_t b3) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {d0, d1, d2, d3};
+    cuuint64_t strides[3] = {s1, s2, s3};
+    cuuint32_t box[4] = {128, b1, b2, b3};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // 4-D tensor map with 128-byte swizzle for TMA stores of 128-byte rows: element type bf16
 // or fp32 (esize 2 or 4); strides in elements for dims 1..3.
 bool make_tmap_4d_plain(CUtensorMap* m, void* base, int esize, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
@@ -98,9 +116,9 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, uint64_t d0, uint64_t rows
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (kernel slot, device).
 bool set_smem_attr_once(const void* fn, int bytes, int slot) {
     static std::mutex mu;
-    static bool done[16][64] = {};
+    static bool done[24][64] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || slot < 0 || slot >= 16) return false;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || slot < 0 || slot >= 24) return false;
     std::lock_guard<std::mutex> g(mu);
     if (done[slot][dev]) return true;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
@@ -353,6 +371,58 @@ namespace {
 
 // hca_decode and hca_decode_vha: the split kernel, then the combine kernel (merge, gate and,
 // with factors, Virtual Head Attention).
+// The split pass (decode.cuh) over a cache, window and workspace whose arguments have been checked; fills in the
+// launch's parameters (p.skip, p.pad and what only the second pass reads are the caller's).
+hca_status_t split_pass(hca::DecodeParams& p, const void* q, const void* kc, const void* vc, const int* page_table,
+                        int page_size, int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
+                        const float* gq, const float* gk, float eps, uint8_t* ws, const DecodeWs& lay, int nsplit, int B,
+                        int Hq, int Hkv, int blk, int W, int Nmax, float scale, unsigned flags, cudaStream_t s) {
+    using namespace hca;
+    const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM;
+    const uint64_t hd = (uint64_t)Hkv * kDecD;
+    CUtensorMap tq, tk, tv, tkw, tvw;
+    bool ok = true;
+    // queries [B, Hq, 512]: a box of 64 heads starting at the group's first head
+    ok &= make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
+    if (paged) {
+        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
+        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
+    } else {
+        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
+        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
+    }
+    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    if (!ok) return HCA_ERR_CUDA;
+
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.seqlens = seqlens;
+    p.page_table = paged ? page_table : nullptr;
+    p.gq = norm ? gq : nullptr;
+    p.gk = norm ? gk : nullptr;
+    p.total = reinterpret_cast<long long*>(ws);
+    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
+    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
+    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
+    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    p.flags = (int)flags; p.nsplit = nsplit;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.eps = eps;
+
+    // compile-time variants: QK normalisation x paged cache
+    using SplitFn = void (*)(const DecodeParams, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                             const CUtensorMap, const CUtensorMap);
+    const SplitFn split = norm ? (paged ? decode_split_kernel<true, true> : decode_split_kernel<true, false>)
+                               : (paged ? decode_split_kernel<false, true> : decode_split_kernel<false, false>);
+    if (!set_smem_attr_once(reinterpret_cast<const void*>(split), (int)kDecSmemBytes, 4 + 2 * norm + paged))
+        return HCA_ERR_CUDA;
+    split<<<nsplit, kDecThreads, kDecSmemBytes, s>>>(p, tq, tk, tv, tkw, tvw);
+    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+    return HCA_OK;
+}
+
 hca_status_t decode_impl(const void* q, const void* kc, const void* vc, const int* page_table, int page_size,
                          int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
                          const float* gq, const float* gk, float eps, const void* gate, float* out,
@@ -397,55 +467,16 @@ hca_status_t decode_impl(const void* q, const void* kc, const void* vc, const in
     const DecodeWs lay = decode_ws_layout(U, nsplit);
     if (ws_bytes < lay.bytes) return HCA_ERR_INVALID_ARG;
 
-    const uint64_t hd = (uint64_t)Hkv * kDecD;
-    CUtensorMap tq, tk, tv, tkw, tvw;
-    bool ok = true;
-    // queries [B, Hq, 512]: a box of 64 heads starting at the group's first head
-    ok &= make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
-    if (paged) {
-        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
-        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
-    } else {
-        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
-        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
-    }
-    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    if (!ok) return HCA_ERR_CUDA;
-
-    DecodeParams p;
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.seqlens = seqlens;
-    p.page_table = paged ? page_table : nullptr;
-    p.gq = norm ? gq : nullptr;
-    p.gk = norm ? gk : nullptr;
+    DecodeParams p = {};
     p.gate = gated ? static_cast<const __nv_bfloat16*>(gate) : nullptr;
     p.out = out;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.total = reinterpret_cast<long long*>(ws);
-    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
-    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
-    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
-    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
     p.vha_u = vha_u;
     p.vha_v = vha_v;
     p.vha_r = vha_u ? vha_r : 0;
-    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
-    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
-    p.flags = (int)flags; p.nsplit = nsplit;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.eps = eps;
-
-    // compile-time variants: QK normalisation x paged cache
-    using SplitFn = void (*)(const DecodeParams, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                             const CUtensorMap, const CUtensorMap);
-    const SplitFn split = norm ? (paged ? decode_split_kernel<true, true> : decode_split_kernel<true, false>)
-                               : (paged ? decode_split_kernel<false, true> : decode_split_kernel<false, false>);
-    if (!set_smem_attr_once(reinterpret_cast<const void*>(split), (int)kDecSmemBytes, 4 + 2 * norm + paged))
-        return HCA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    split<<<nsplit, kDecThreads, kDecSmemBytes, s>>>(p, tq, tk, tv, tkw, tvw);
-    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+    const hca_status_t st = split_pass(p, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps,
+                                       static_cast<uint8_t*>(workspace), lay, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
+    if (st != HCA_OK) return st;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)U, (unsigned)(kDecD / kMergeCh));
@@ -1005,4 +1036,227 @@ extern "C" hca_status_t hca_dsa_attend(const void* q, const void* k, const void*
         }
     }
     return HCA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// The 8-bit compressed cache (quant.cuh, decode_quant.cuh).
+namespace {
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool pool_dim(int x) { return x == 64 || x == 128 || x == 256 || x == 512; }
+
+// Checks of a contiguous or paged cache's geometry, shared by the calls below.
+bool cache_geometry(bool paged, const int* page_table, int page_size, int max_pages, int num_pages, int Nmax) {
+    if (paged)
+        return page_table && aligned4(page_table) && page_size >= 64 && page_size % 64 == 0 && max_pages >= 1 &&
+               num_pages >= 1 && (long long)max_pages * page_size <= 0x7fffffffLL;
+    return Nmax >= 1;
+}
+
+// The merge pass after the passes that wrote the records; it may start while they still run.
+hca_status_t launch_merge(const hca::MergeParams& mp, bool prefix, cudaStream_t s) {
+    using namespace hca;
+    const long long U = (long long)mp.B * mp.Hkv;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)U, (unsigned)(kDecD / kMergeCh));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = mp.vha_u ? combine_vha_smem(mp.vha_r) : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // records loaded per round, from the average number of pieces per unit (about nsplit / U)
+    const bool wide = (long long)mp.nsplit >= 3 * U;
+    using Fn = void (*)(const MergeParams);
+    const Fn fns[2][2][2] = {{{merge_kernel<2, false, false>, merge_kernel<2, false, true>},
+                              {merge_kernel<2, true, false>, merge_kernel<2, true, true>}},
+                             {{merge_kernel<4, false, false>, merge_kernel<4, false, true>},
+                              {merge_kernel<4, true, false>, merge_kernel<4, true, true>}}};
+    if (cudaLaunchKernelEx(&cfg, fns[wide][mp.vha_u != nullptr][prefix], mp) != cudaSuccess) {
+        cudaGetLastError();
+        return HCA_ERR_CUDA;
+    }
+    return HCA_OK;
+}
+
+}  // namespace
+
+extern "C" hca_status_t hca_compress_quant(const void* k, const void* v, const float* w, void* kc, void* vc,
+                                           void* scales, int B, int T, int Hkv, int d, int dv, int blk,
+                                           hca_stream_t stream) {
+    if (B < 0 || T < 0 || Hkv < 1 || blk < 1) return HCA_ERR_INVALID_ARG;
+    if (!pool_dim(d) || !pool_dim(dv) || blk > 128) return HCA_ERR_UNSUPPORTED;
+    const int64_t Nc = T / blk;
+    const int64_t entries = (int64_t)B * Nc * Hkv;
+    if (entries == 0) return HCA_OK;
+    if (entries > 0x7fffffffLL) return HCA_ERR_INVALID_ARG;
+    if (!k || !v || !kc || !vc || !scales) return HCA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(vc) || !aligned2(scales) || (w && !aligned4(w)))
+        return HCA_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    using Fn = void (*)(const __nv_bfloat16*, const __nv_bfloat16*, const float*, uint8_t*, uint8_t*, uint16_t*, int, int,
+                        int, int);
+    auto index = [](int x) { return x == 64 ? 0 : x == 128 ? 1 : x == 256 ? 2 : 3; };
+#define HCA_CQ_ROW(DK)                                                            \
+    {hca::compress_quant_kernel<DK, 64>, hca::compress_quant_kernel<DK, 128>,    \
+     hca::compress_quant_kernel<DK, 256>, hca::compress_quant_kernel<DK, 512>}
+    static const Fn fns[4][4] = {HCA_CQ_ROW(64), HCA_CQ_ROW(128), HCA_CQ_ROW(256), HCA_CQ_ROW(512)};
+#undef HCA_CQ_ROW
+    fns[index(d)][index(dv)]<<<(unsigned)entries, hca::kCompressThreads, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), w, static_cast<uint8_t*>(kc),
+        static_cast<uint8_t*>(vc), static_cast<uint16_t*>(scales), T, Hkv, blk, (int)Nc);
+    return launch_status();
+}
+
+extern "C" hca_status_t hca_append_quant(const void* k_new, const void* v_new, const float* w_new, const int* seqlens,
+                                         void* kw, void* vw, void* kc, void* vc, void* scales, const int* page_table,
+                                         int page_size, int max_pages, int num_pages, void* state, int B, int Hkv, int d,
+                                         int dv, int blk, int W, int Nmax, unsigned flags, hca_stream_t stream) {
+    if (B < 0 || Hkv < 1 || blk < 1 || W < 1) return HCA_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)HCA_PAGED) return HCA_ERR_UNSUPPORTED;
+    if (!pool_dim(d) || !pool_dim(dv) || blk > 128) return HCA_ERR_UNSUPPORTED;
+    if (B == 0) return HCA_OK;
+    if ((long long)B * Hkv > 0x7fffffffLL) return HCA_ERR_INVALID_ARG;
+    const bool paged = flags & HCA_PAGED;
+    if (!k_new || !v_new || !seqlens || !kw || !vw || !kc || !vc || !scales || !state) return HCA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(kw) || !aligned16(vw) || !aligned16(kc) || !aligned16(vc) ||
+        !aligned2(scales) || !aligned16(state) || !aligned4(seqlens) || (w_new && !aligned4(w_new)))
+        return HCA_ERR_INVALID_ARG;
+    if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    hca::AppendQuantParams p;
+    p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    p.w = w_new;
+    p.seqlens = seqlens;
+    p.kw = static_cast<__nv_bfloat16*>(kw);
+    p.vw = static_cast<__nv_bfloat16*>(vw);
+    p.kc = static_cast<uint8_t*>(kc);
+    p.vc = static_cast<uint8_t*>(vc);
+    p.sc = static_cast<uint16_t*>(scales);
+    p.page_table = paged ? page_table : nullptr;
+    p.state = static_cast<float*>(state);
+    p.B = B; p.Hkv = Hkv; p.d = d; p.dv = dv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    hca::append_quant_kernel<<<(unsigned)(B * Hkv), hca::kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launch_status();
+}
+
+extern "C" hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales, const int* page_table,
+                                       int page_size, int max_pages, int num_pages, const int* counts, void* k, void* v,
+                                       int B, int n, int Hkv, int d, int dv, int Nmax, unsigned flags,
+                                       hca_stream_t stream) {
+    if (B < 0 || n < 0 || Hkv < 1) return HCA_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)HCA_PAGED) return HCA_ERR_UNSUPPORTED;
+    if (!pool_dim(d) || !pool_dim(dv)) return HCA_ERR_UNSUPPORTED;
+    if ((long long)B * n == 0) return HCA_OK;
+    const bool paged = flags & HCA_PAGED;
+    if (!kc || !vc || !scales || !counts || !k || !v) return HCA_ERR_INVALID_ARG;
+    if (!aligned16(kc) || !aligned16(vc) || !aligned2(scales) || !aligned4(counts) || !aligned16(k) || !aligned16(v))
+        return HCA_ERR_INVALID_ARG;
+    if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    const int ns = hca::num_sms();
+    if (ns <= 0) return HCA_ERR_CUDA;
+    hca::ReadQuantParams p;
+    p.kc = static_cast<const uint8_t*>(kc);
+    p.vc = static_cast<const uint8_t*>(vc);
+    p.sc = static_cast<const uint16_t*>(scales);
+    p.page_table = paged ? page_table : nullptr;
+    p.counts = counts;
+    p.k = static_cast<__nv_bfloat16*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
+    p.B = B; p.n = n; p.Hkv = Hkv; p.d = d; p.dv = dv; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    p.items = (long long)B * n * Hkv;
+    const long long need = (p.items + hca::kReadThreads / 32 - 1) / (hca::kReadThreads / 32);
+    const long long grid = std::min<long long>(need, 8LL * ns);
+    hca::read_quant_kernel<<<(unsigned)grid, hca::kReadThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launch_status();
+}
+
+extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, const void* scales,
+                                         const int* page_table, int page_size, int max_pages, int num_pages,
+                                         const void* kw, const void* vw, const int* seqlens, const float* gq,
+                                         const float* gk, float eps, const void* gate, const float* vha_u,
+                                         const float* vha_v, int vha_rank, void* out, void* workspace, size_t ws_bytes,
+                                         int B, int Hq, int Hkv, int d, int dv, int blk, int W, int Nmax, float scale,
+                                         unsigned flags, hca_stream_t stream) {
+    using namespace hca;
+    if (B < 0 || Hq < 1 || Hkv < 1 || blk < 1 || W < 1) return HCA_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)(HCA_QK_NORM | HCA_OUT_GATE | HCA_PAGED | HCA_WINDOW_RING | HCA_OUT_F32))
+        return HCA_ERR_UNSUPPORTED;
+    if (d != kDecD || dv != kDecD || Hq % Hkv != 0 || Hq / Hkv > kDecHeads || blk > 128) return HCA_ERR_UNSUPPORTED;
+    if (!(scale == scale) || !(eps >= 0.f)) return HCA_ERR_INVALID_ARG;
+    if (B == 0) return HCA_OK;
+    const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM, gated = flags & HCA_OUT_GATE;
+    if (!q || !kc || !vc || !scales || !kw || !vw || !seqlens || !out || !workspace) return HCA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned2(scales) || !aligned16(kw) || !aligned16(vw) ||
+        !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
+        return HCA_ERR_INVALID_ARG;
+    if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    if (norm && (!gq || !gk || !aligned4(gq) || !aligned4(gk))) return HCA_ERR_INVALID_ARG;
+    if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
+    if (vha_u || vha_v) {
+        if (!vha_u || !vha_v || vha_rank < 1 || !aligned4(vha_u) || !aligned4(vha_v)) return HCA_ERR_INVALID_ARG;
+        if (Hkv != 1 || vha_rank > kDecVhaMaxRank) return HCA_ERR_UNSUPPORTED;
+    }
+    const int nsplit = num_sms();
+    if (nsplit <= 0) return HCA_ERR_CUDA;
+    const long long U = (long long)B * Hkv;
+    if (U > (1 << 24)) return HCA_ERR_INVALID_ARG;
+    const DecodeWs lay = decode_ws_layout(U, nsplit);
+    if (ws_bytes < lay.bytes) return HCA_ERR_INVALID_ARG;
+
+    const uint64_t hd = (uint64_t)Hkv * kDecD;
+    CUtensorMap tq, tk, tv, tkw, tvw;
+    bool ok = make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
+    const uint64_t rows = paged ? page_size : Nmax, outer = paged ? num_pages : B;
+    const uint32_t box = paged ? 64 : 128;
+    ok &= make_tmap_4d_u8(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+    ok &= make_tmap_4d_u8(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    if (!ok) return HCA_ERR_CUDA;
+
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    QuantParams p;
+    p.seqlens = seqlens;
+    p.page_table = paged ? page_table : nullptr;
+    p.sc = static_cast<const uint16_t*>(scales);
+    p.gq = norm ? gq : nullptr;
+    p.gk = norm ? gk : nullptr;
+    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
+    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
+    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
+    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    p.flags = (int)flags; p.nsplit = nsplit;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.eps = eps;
+    using Fn = void (*)(const QuantParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                        const CUtensorMap);
+    const Fn fn = norm ? (paged ? decode_quant_kernel<true, true> : decode_quant_kernel<true, false>)
+                       : (paged ? decode_quant_kernel<false, true> : decode_quant_kernel<false, false>);
+    if (!set_smem_attr_once(reinterpret_cast<const void*>(fn), (int)kQdSmem, 16 + 2 * norm + paged)) return HCA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    fn<<<nsplit, kQdThreads, kQdSmem, s>>>(p, tq, tk, tv, tkw, tvw);
+    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+
+    MergeParams mp = {};
+    mp.seqlens = seqlens;
+    mp.meta = p.meta;
+    mp.rec_m = p.rec_m;
+    mp.rec_l = p.rec_l;
+    mp.rec_o = p.rec_o;
+    mp.gate = gated ? static_cast<const __nv_bfloat16*>(gate) : nullptr;
+    mp.vha_u = vha_u;
+    mp.vha_v = vha_v;
+    mp.vha_r = vha_u ? vha_rank : 0;
+    mp.out = out;
+    mp.B = B; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = p.G; mp.nsplit = nsplit;
+    mp.out_f32 = (flags & HCA_OUT_F32) ? 1 : 0;
+    return launch_merge(mp, false, s);
 }

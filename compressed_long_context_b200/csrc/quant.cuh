@@ -1,0 +1,296 @@
+// quant.cuh -- the 8-bit compressed cache: written from raw tokens (hca_compress_quant), one token at a
+// time (hca_append_quant), and read back to bf16 (hca_read_quant).  The format is in fp8.cuh.
+//
+// The pooled entry stays in fp32 until it is quantised: one rounding, to e4m3.
+#pragma once
+
+#include "append.cuh"
+#include "compress.cuh"
+#include "fp8.cuh"
+
+namespace hca {
+
+// Largest magnitude over the CTA's threads (every thread calls it; scratch: one float per warp).
+template <int THREADS>
+__device__ __forceinline__ float block_amax(float a, float* scratch) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = scratch[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) a = fmaxf(a, scratch[w]);
+    return a;
+}
+
+// ------------------------------------------------------------------ compress
+
+// Softmax of a block's pooling weights (all zero without weights) by one warp, as in compress.cuh.
+__device__ __forceinline__ void block_alpha(const float* __restrict__ w, int64_t pos0, int blk, float* alpha) {
+    const int lane = threadIdx.x & 31;
+    float wv[4];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int idx = lane + 32 * i;
+        wv[i] = idx < blk ? (w ? w[pos0 + idx] : 0.f) : -INFINITY;
+        m = fmaxf(m, wv[i]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        wv[i] = (lane + 32 * i) < blk ? expf(wv[i] - m) : 0.f;
+        s += wv[i];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (lane + 32 * i < blk) alpha[lane + 32 * i] = wv[i] * inv;
+}
+
+// Weighted sum over `blk` rows of one tensor with D channels, then the codes of the pooled vector.
+// Returns the scale byte.
+template <int D>
+__device__ __forceinline__ uint32_t pool_rows_quant(const __nv_bfloat16* __restrict__ src, int64_t row_stride,
+                                                    const float* __restrict__ alpha, int blk,
+                                                    float* __restrict__ red, float* __restrict__ scratch,
+                                                    uint8_t* __restrict__ dst) {
+    constexpr int TPR = D / 8;                   // threads per row (16 bytes each)
+    constexpr int R = kCompressThreads / TPR;    // rows in flight per pass
+    const int tid = threadIdx.x;
+    const int c0 = (tid % TPR) * 8;
+    const int r0 = tid / TPR;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int r = r0; r < blk; r += R * kCompressUnroll) {
+        uint4 x[kCompressUnroll];
+#pragma unroll
+        for (int u = 0; u < kCompressUnroll; ++u) {
+            const int rr = r + u * R;
+            if (rr < blk) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + rr * row_stride + c0));
+        }
+#pragma unroll
+        for (int u = 0; u < kCompressUnroll; ++u) {
+            const int rr = r + u * R;
+            if (rr < blk) {
+                const float a = alpha[rr];
+                acc[0] = fmaf(a, bf16lo(x[u].x), acc[0]);
+                acc[1] = fmaf(a, bf16hi(x[u].x), acc[1]);
+                acc[2] = fmaf(a, bf16lo(x[u].y), acc[2]);
+                acc[3] = fmaf(a, bf16hi(x[u].y), acc[3]);
+                acc[4] = fmaf(a, bf16lo(x[u].z), acc[4]);
+                acc[5] = fmaf(a, bf16hi(x[u].z), acc[5]);
+                acc[6] = fmaf(a, bf16lo(x[u].w), acc[6]);
+                acc[7] = fmaf(a, bf16hi(x[u].w), acc[7]);
+            }
+        }
+    }
+    float4* o = reinterpret_cast<float4*>(red + r0 * D + c0);
+    o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    __syncthreads();
+    // two channels per thread; D / 2 <= kCompressThreads
+    float s0 = 0.f, s1 = 0.f;
+    const bool mine = tid < D / 2;
+    if (mine) {
+#pragma unroll 4
+        for (int r = 0; r < R; ++r) {
+            const float2 p = *reinterpret_cast<const float2*>(red + r * D + 2 * tid);
+            s0 += p.x;
+            s1 += p.y;
+        }
+    }
+    const uint32_t byte = q_scale_byte(block_amax<kCompressThreads>(fmaxf(q_mag(s0), q_mag(s1)), scratch));
+    const float inv = q_inv_scale(byte);
+    if (mine) reinterpret_cast<uint16_t*>(dst)[tid] = (uint16_t)cvt_e4m3x2(q_prep(s0, inv), q_prep(s1, inv));
+    __syncthreads();
+    return byte;
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kCompressThreads)
+compress_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                      const float* __restrict__ w, uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
+                      uint16_t* __restrict__ sc, int T, int Hkv, int blk, int Nc) {
+    __shared__ float alpha[128];
+    __shared__ __align__(16) float red[kCompressThreads * 8];
+    __shared__ float scratch[kCompressThreads / 32];
+    const int e = blockIdx.x;                 // entry index, KV head fastest
+    const int g = e % Hkv;
+    const int bj = e / Hkv;
+    const int j = bj % Nc;
+    const int b = bj / Nc;
+    const int64_t pos0 = (int64_t)b * T + (int64_t)blk * j;
+    if (threadIdx.x < 32) block_alpha(w, pos0, blk, alpha);
+    __syncthreads();
+    const uint32_t kb = pool_rows_quant<DK>(k + (pos0 * Hkv + g) * DK, (int64_t)Hkv * DK, alpha, blk, red, scratch,
+                                            kc + (int64_t)e * DK);
+    const uint32_t vb = pool_rows_quant<DV>(v + (pos0 * Hkv + g) * DV, (int64_t)Hkv * DV, alpha, blk, red, scratch,
+                                            vc + (int64_t)e * DV);
+    if (threadIdx.x == 0) sc[e] = (uint16_t)(kb | vb << 8);
+}
+
+// ------------------------------------------------------------------ append
+
+struct AppendQuantParams {
+    const __nv_bfloat16* k_new;   // [B, Hkv, d]
+    const __nv_bfloat16* v_new;   // [B, Hkv, dv]
+    const float* w;               // [B] or null (weight 0)
+    const int* seqlens;           // [B], length including the new token; 0: a padding row
+    __nv_bfloat16* kw;            // [B, W, Hkv, d] ring
+    __nv_bfloat16* vw;
+    uint8_t* kc;                  // [B, Nmax, Hkv, d] codes or pool [P, ps, Hkv, d]
+    uint8_t* vc;
+    uint16_t* sc;                 // [B, Nmax, Hkv] or [P, ps, Hkv] scale pairs
+    const int* page_table;        // [B, max_pages] or null
+    float* state;                 // [B, Hkv, kAppendHeader + d + dv]
+    int B, Hkv, d, dv, blk, W, Nmax, page_size, max_pages, num_pages;
+};
+
+// One CTA per (sequence, KV head), thread i owns channels 4i .. 4i+3 of K and of V, as append_kernel;
+// every load is issued before any result is needed, so a call costs one memory round trip.  Completing a
+// block adds two block-wide maxima.
+__global__ void __launch_bounds__(kAppendThreads) append_quant_kernel(const AppendQuantParams p) {
+    __shared__ float scratch[2][kAppendThreads / 32];
+    const int u = blockIdx.x;
+    const int b = u / p.Hkv, g = u - b * p.Hkv;
+    const int c = 4 * threadIdx.x;
+    const bool hk = c < p.d, hv = c < p.dv;
+    float* st = p.state + (size_t)u * (kAppendHeader + p.d + p.dv);
+    float* acc_k = st + kAppendHeader;
+    float* acc_v = st + kAppendHeader + p.d;
+    const int L = __ldg(p.seqlens + b);
+    const float w = p.w ? __ldg(p.w + b) : 0.f;
+    const float2 ms = *reinterpret_cast<const float2*>(st);
+    const uint2 xk = hk ? *reinterpret_cast<const uint2*>(p.k_new + (size_t)u * p.d + c) : make_uint2(0u, 0u);
+    const uint2 xv = hv ? *reinterpret_cast<const uint2*>(p.v_new + (size_t)u * p.dv + c) : make_uint2(0u, 0u);
+    float4 tk = hk ? *reinterpret_cast<const float4*>(acc_k + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 tv = hv ? *reinterpret_cast<const float4*>(acc_v + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (L < 1) {
+        if (L < 0 && threadIdx.x == 0) record_error(HCA_ERR_DEVICE_INPUT);
+        return;
+    }
+    const long long pos = (long long)L - 1;
+    const int slot = (int)(pos % p.W);
+    const float m_old = ms.x, s_old = ms.y;
+    // a weight of -inf adds nothing, also as a block's first; NaN stays in the sum until the block is complete
+    const bool empty = s_old == 0.f;
+    const float m_new = empty ? w : fmaxf(m_old, w);
+    const float a = empty ? 0.f : expf(m_old - m_new);
+    const float e = w == -INFINITY ? 0.f : expf(w - m_new);
+    const float s_new = fmaf(s_old, a, e);
+    const bool complete = (pos + 1) % p.blk == 0;
+    auto fold = [&](uint2 x, float4& t) {
+        t.x = fmaf(e, bf16lo(x.x), t.x * a);
+        t.y = fmaf(e, bf16hi(x.x), t.y * a);
+        t.z = fmaf(e, bf16lo(x.y), t.z * a);
+        t.w = fmaf(e, bf16hi(x.y), t.w * a);
+    };
+    const size_t ring = ((size_t)b * p.W + slot) * p.Hkv + g;
+    fold(xk, tk);
+    fold(xv, tv);
+    if (hk) *reinterpret_cast<uint2*>(p.kw + ring * p.d + c) = xk;
+    if (hv) *reinterpret_cast<uint2*>(p.vw + ring * p.dv + c) = xv;
+    if (complete) {
+        const float inv_s = 1.f / s_new;
+        const float4 ek = make_float4(tk.x * inv_s, tk.y * inv_s, tk.z * inv_s, tk.w * inv_s);
+        const float4 ev = make_float4(tv.x * inv_s, tv.y * inv_s, tv.z * inv_s, tv.w * inv_s);
+        auto amax4 = [](float4 x) { return fmaxf(fmaxf(q_mag(x.x), q_mag(x.y)), fmaxf(q_mag(x.z), q_mag(x.w))); };
+        const uint32_t kb = q_scale_byte(block_amax<kAppendThreads>(hk ? amax4(ek) : 0.f, scratch[0]));
+        const uint32_t vb = q_scale_byte(block_amax<kAppendThreads>(hv ? amax4(ev) : 0.f, scratch[1]));
+        // the entry's row (none: out of the cache, reported)
+        const long long j = pos / p.blk;
+        long long row = -1;
+        if (p.page_table) {
+            const long long pi = j / p.page_size;
+            if (pi < p.max_pages) {
+                const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + pi);
+                if (pg >= 0 && pg < p.num_pages) row = (long long)pg * p.page_size + j % p.page_size;
+            }
+        } else if (j < p.Nmax) {
+            row = (long long)b * p.Nmax + j;
+        }
+        if (row >= 0) {
+            const size_t rg = (size_t)row * p.Hkv + g;
+            if (hk) *reinterpret_cast<uint32_t*>(p.kc + rg * p.d + c) = q_codes4(ek, q_inv_scale(kb));
+            if (hv) *reinterpret_cast<uint32_t*>(p.vc + rg * p.dv + c) = q_codes4(ev, q_inv_scale(vb));
+            if (threadIdx.x == 0) p.sc[rg] = (uint16_t)(kb | vb << 8);
+        } else if (threadIdx.x == 0) {
+            record_error(HCA_ERR_DEVICE_INPUT);
+        }
+        tk = tv = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (hk) *reinterpret_cast<float4*>(acc_k + c) = tk;
+    if (hv) *reinterpret_cast<float4*>(acc_v + c) = tv;
+    __syncthreads();      // every thread has read m and s
+    if (threadIdx.x == 0) *reinterpret_cast<float2*>(st) = complete ? make_float2(0.f, 0.f) : make_float2(m_new, s_new);
+}
+
+// ------------------------------------------------------------------ read back
+
+struct ReadQuantParams {
+    const uint8_t* kc;            // [B, Nmax, Hkv, d] codes or pool [P, ps, Hkv, d]
+    const uint8_t* vc;
+    const uint16_t* sc;
+    const int* page_table;        // [B, max_pages] or null
+    const int* counts;            // [B] entries to read
+    __nv_bfloat16* k;             // [B, n, Hkv, d]
+    __nv_bfloat16* v;
+    int B, n, Hkv, d, dv, Nmax, page_size, max_pages, num_pages;
+    long long items;              // B * n * Hkv
+};
+
+constexpr int kReadThreads = 256;
+
+// One warp per (sequence, entry, KV head): 16 codes per lane and step, two 16-byte stores.  Entries at and
+// past counts[b] are left as they are.
+__global__ void __launch_bounds__(kReadThreads) read_quant_kernel(const ReadQuantParams p) {
+    const int lane = threadIdx.x & 31;
+    const long long nw = (long long)gridDim.x * (kReadThreads / 32);
+    for (long long i = (long long)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5); i < p.items; i += nw) {
+        const int g = (int)(i % p.Hkv);
+        const long long bj = i / p.Hkv;
+        const int j = (int)(bj % p.n);
+        const int b = (int)(bj / p.n);
+        const long long cap = p.page_table ? (long long)p.max_pages * p.page_size : (long long)p.Nmax;
+        const int cnt = __ldg(p.counts + b);
+        if ((cnt < 0 || cnt > p.n || cnt > cap) && j == 0 && lane == 0) record_error(HCA_ERR_DEVICE_INPUT);
+        if (j >= cnt || j >= cap) continue;
+        long long row = (long long)b * p.Nmax + j;
+        if (p.page_table) {
+            const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + j / p.page_size);
+            if (pg < 0 || pg >= p.num_pages) {
+                if (lane == 0) record_error(HCA_ERR_DEVICE_INPUT);
+                continue;
+            }
+            row = (long long)pg * p.page_size + j % p.page_size;
+        }
+        const size_t rg = (size_t)row * p.Hkv + g;
+        const uint32_t sc = __ldg(p.sc + rg);
+        auto widen = [&](const uint8_t* src, __nv_bfloat16* dst, int D, float s) {
+            for (int c = 16 * lane; c < D; c += 512) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + c));
+                const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 a = e4m3x2_f32(w4[q] & 0xffffu), b2 = e4m3x2_f32(w4[q] >> 16);
+                    y[2 * q] = pack_bf16x2(a.x * s, a.y * s);
+                    y[2 * q + 1] = pack_bf16x2(b2.x * s, b2.y * s);
+                }
+                uint4* o = reinterpret_cast<uint4*>(dst + c);
+                o[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+        };
+        widen(p.kc + rg * p.d, p.k + (size_t)i * p.d, p.d, q_scale(sc & 0xffu));
+        widen(p.vc + rg * p.dv, p.v + (size_t)i * p.dv, p.dv, q_scale(sc >> 8));
+    }
+}
+
+}  // namespace hca

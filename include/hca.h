@@ -362,6 +362,67 @@ hca_status_t hca_append(const void* k_new, const void* v_new, const float* w_new
 hca_status_t hca_gate_logits(const void* cq, const void* wg, void* gate, int n, int rq, int Hq, int dv,
                              hca_stream_t stream);
 
+/*
+ * The 8-bit compressed cache: entries as e4m3 codes with power-of-two scales (no counterpart in the
+ * pages; the cache takes 1026 instead of 2048 bytes per 512-dim entry).
+ *
+ * Format of an entry (row, KV head): d codes of the key, dv of the value, one byte each (e4m3, no
+ * infinity, 0x7f / 0xff are NaN), and two scale bytes (e8m0: byte u stands for 2^(u - 127)), key first:
+ *   kc [.., Hkv, d], vc [.., Hkv, dv]  codes;   scales [.., Hkv, 2]
+ * The value of a code c is c * 2^e.  e is the smallest integer with max|x| <= 448 * 2^e over the vector,
+ * clamped to [-64, 120]; the maximum is over finite values, and a value that is not finite is stored
+ * as NaN.  Codes are rounded to nearest even from the fp32 pooled entry (one rounding): off by at most
+ * max(2^-4 |x|, 2^(e - 10)).  Readers accept the scales these calls write: powers of two in that range.
+ *
+ * hca_compress_quant -- hca_compress into the 8-bit form.  k, v, w as for hca_compress;
+ *   kc [B,Nc,Hkv,d], vc [B,Nc,Hkv,dv] codes (16-byte aligned), scales [B,Nc,Hkv,2] (2-byte aligned).
+ * Supported and errors: as hca_compress.
+ */
+hca_status_t hca_compress_quant(const void* k, const void* v, const float* w, void* kc, void* vc, void* scales,
+                                int B, int T, int Hkv, int d, int dv, int blk, hca_stream_t stream);
+
+/*
+ * hca_append_quant -- hca_append into the 8-bit form: the newest token enters the bf16 window ring and
+ * the fp32 pool; a block it completes becomes one 8-bit entry.  kc, vc, scales: [B,Nmax,Hkv,..], or page
+ * pools [P,page_size,Hkv,..] with HCA_PAGED; the state (hca_append_state_size) and every other argument
+ * as for hca_append.  seqlens[b] == 0 marks a padding row: nothing of it is read or written.
+ */
+hca_status_t hca_append_quant(const void* k_new, const void* v_new, const float* w_new, const int* seqlens,
+                              void* kw, void* vw, void* kc, void* vc, void* scales,
+                              const int* page_table, int page_size, int max_pages, int num_pages,
+                              void* state, int B, int Hkv, int d, int dv, int blk, int W, int Nmax,
+                              unsigned flags, hca_stream_t stream);
+
+/*
+ * hca_read_quant -- entries 0 .. counts[b] - 1 of every sequence back in bf16 (exact: a code has 4
+ * significant bits).  k [B,n,Hkv,d], v [B,n,Hkv,dv] bf16 outputs; rows at and past counts[b] are left as
+ * they are.  counts [B] int32 (device), 0 <= counts[b] <= n and within the cache (Nmax, or the row of the
+ * page table): else HCA_ERR_DEVICE_INPUT, and the rows outside are not read or written.
+ * Supported: d, dv in {64, 128, 256, 512}; flags 0 or HCA_PAGED (page_size a multiple of 64).
+ */
+hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales,
+                            const int* page_table, int page_size, int max_pages, int num_pages,
+                            const int* counts, void* k, void* v,
+                            int B, int n, int Hkv, int d, int dv, int Nmax, unsigned flags, hca_stream_t stream);
+
+/*
+ * hca_decode_quant -- hca_decode over an 8-bit compressed cache and a raw bf16 window: the attention of
+ * the entries' values code * 2^e.  kc, vc, scales contiguous [B,Nmax,Hkv,..] or page pools with HCA_PAGED;
+ * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v [Hq, vha_rank] fp32 for the mixing of
+ * hca_decode_vha (Hkv == 1), else NULL; every other argument, the workspace (hca_decode_workspace_size)
+ * and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row: its output is zero.
+ * Arithmetic: codes go to the tensor cores as they are; the query and the probabilities are split into
+ * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.
+ */
+hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, const void* scales,
+                              const int* page_table, int page_size, int max_pages, int num_pages,
+                              const void* kw, const void* vw, const int* seqlens,
+                              const float* gq, const float* gk, float eps, const void* gate,
+                              const float* vha_u, const float* vha_v, int vha_rank,
+                              void* out, void* workspace, size_t ws_bytes,
+                              int B, int Hq, int Hkv, int d, int dv, int blk, int W, int Nmax,
+                              float scale, unsigned flags, hca_stream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* hca_status_string(hca_status_t status);
 
