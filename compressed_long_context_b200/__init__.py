@@ -18,7 +18,7 @@ from ._lib import (HCA_OUT_F32, HCA_OUT_GATE, HCA_PAGED, HCA_QK_NORM,  # noqa: F
 
 __all__ = ["HCAError", "compress", "prefill", "decode", "decode_workspace_size", "append", "append_state_size",
            "vha", "gate_logits", "prefill_backward", "dsa_index", "dsa_topk", "dsa_attend", "dsa_decode",
-           "compress_quant", "append_quant", "read_quant", "decode_quant",
+           "compress_quant", "append_quant", "read_quant", "decode_quant", "decode_shared", "decode_shared_workspace_size",
            "get_device_error", "status_string"]
 
 
@@ -561,4 +561,57 @@ def decode_quant(q, kc, vc, sc, kw, vw, seqlens, blk, W, scale, page_table=None,
     _run("hca_decode_quant", dev, _p(q), _p(kc), _p(vc), _p(sc), _p(page_table), page_size, max_pages, num_pages, _p(kw),
          _p(vw), _p(seqlens), _p(gq), _p(gk), float(eps), _p(gate), _p(vha_u), _p(vha_v), r, _p(out), _p(workspace),
          workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Nmax, float(scale), flags)
+    return out
+
+
+def decode_shared_workspace_size(B, Hq, Hkv, dv, Np):
+    return _lib.load().hca_decode_shared_workspace_size(B, Hq, Hkv, dv, Np)
+
+
+def decode_shared(q, kp, vp, kc, vc, kw, vw, seqlens, blk, W, scale, page_table=None, gq=None, gk=None, eps=1e-6,
+                  gate=None, out=None, workspace=None, window_ring=False, vha_u=None, vha_v=None, out_f32=False):
+    """``decode`` of a batch whose sequences begin with the same compressed entries, held once and attended
+    once for all: kp / vp [Np,Hkv,512] bf16.  kc / vc hold each sequence's entries from the Np-th on (contiguous
+    [B,Nmax,Hkv,512], or page pools with page_table); seqlens count the prefix's tokens too.  Other arguments
+    as for ``decode``.  Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero."""
+    _need(q, torch.bfloat16, "q")
+    dev = q.device
+    for name, t in (("kp", kp), ("vp", vp), ("kc", kc), ("vc", vc), ("kw", kw), ("vw", vw)):
+        _need(t, torch.bfloat16, name, dev)
+    _need(seqlens, torch.int32, "seqlens", dev)
+    B, Hq, d = q.shape
+    Np, Hkv, dv = kp.shape[0], kc.shape[2], vc.shape[3]
+    flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
+    if gq is not None or gk is not None:
+        _need(gq, torch.float32, "gq", dev)
+        _need(gk, torch.float32, "gk", dev)
+        flags |= HCA_QK_NORM
+    if gate is not None:
+        _need(gate, torch.bfloat16, "gate", dev)
+        flags |= HCA_OUT_GATE
+    if window_ring:
+        flags |= HCA_WINDOW_RING
+    if out is None:
+        out = torch.empty((B, Hq, dv), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
+    _need(out, torch.float32 if out_f32 else torch.bfloat16, "out", dev)
+    if out_f32:
+        flags |= HCA_OUT_F32
+    for name, t, n in (("kp", kp, Np * Hkv * d), ("vp", vp, Np * Hkv * dv), ("kc", kc, rows * Hkv * d),
+                       ("vc", vc, rows * Hkv * dv), ("kw", kw, B * W * Hkv * d), ("vw", vw, B * W * Hkv * dv),
+                       ("seqlens", seqlens, B), ("gq", gq, d), ("gk", gk, d), ("gate", gate, B * Hq * dv),
+                       ("out", out, B * Hq * dv)):
+        _room(t, n, name)
+    r = 0
+    if vha_u is not None or vha_v is not None:
+        _need(vha_u, torch.float32, "vha_u", dev)
+        _need(vha_v, torch.float32, "vha_v", dev)
+        r = vha_u.shape[1]
+        if vha_u.shape != (Hq, r) or vha_v.shape != (Hq, r):
+            raise ValueError("vha_u and vha_v must both be [Hq, r]")
+    if workspace is None:
+        workspace = torch.empty((max(decode_shared_workspace_size(B, Hq, Hkv, dv, Np), 1),), dtype=torch.uint8, device=dev)
+    _need(workspace, torch.uint8, "workspace", dev)
+    _run("hca_decode_shared", dev, _p(q), _p(kp), _p(vp), _p(kc), _p(vc), _p(page_table), page_size, max_pages, num_pages,
+         _p(kw), _p(vw), _p(seqlens), _p(gq), _p(gk), float(eps), _p(gate), _p(vha_u), _p(vha_v), r, _p(out), _p(workspace),
+         workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Np, Nmax, float(scale), flags)
     return out

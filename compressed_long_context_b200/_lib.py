@@ -28,7 +28,8 @@ EXPORTS = ("hca_compress", "hca_prefill", "hca_decode_workspace_size", "hca_deco
            "hca_prefill_backward_workspace_size", "hca_prefill_backward", "hca_debug_set_backward_segment",
            "hca_debug_set_dsa_rows_limit",
            "hca_dsa_index", "hca_dsa_topk", "hca_dsa_attend",
-           "hca_compress_quant", "hca_append_quant", "hca_read_quant", "hca_decode_quant")
+           "hca_compress_quant", "hca_append_quant", "hca_read_quant", "hca_decode_quant",
+           "hca_decode_shared", "hca_decode_shared_workspace_size")
 
 _lib = None
 
@@ -94,6 +95,11 @@ def load():
     lib.hca_decode_quant.restype = _i
     lib.hca_decode_quant.argtypes = ([_vp] * 5 + [_i] * 3 + [_vp] * 5 + [_f] + [_vp] * 3 + [_i, _vp, _vp, _sz] + [_i] * 8
                                      + [_f, _u, _vp])
+    lib.hca_decode_shared_workspace_size.restype = _sz
+    lib.hca_decode_shared_workspace_size.argtypes = [_i] * 5
+    lib.hca_decode_shared.restype = _i
+    lib.hca_decode_shared.argtypes = ([_vp] * 6 + [_i] * 3 + [_vp] * 5 + [_f] + [_vp] * 3 + [_i, _vp, _vp, _sz] + [_i] * 9
+                                      + [_f, _u, _vp])
     lib.hca_debug_set_backward_segment.restype = _i
     lib.hca_debug_set_backward_segment.argtypes = [_i]
     lib.hca_debug_set_dsa_rows_limit.restype = _i

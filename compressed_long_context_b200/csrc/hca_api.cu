@@ -18,6 +18,7 @@
 #include "merge.cuh"
 #include "prefill.cuh"
 #include "prefill_pair.cuh"
+#include "prefix.cuh"
 #include "quant.cuh"
 #include "vha.cuh"
 
@@ -369,8 +370,6 @@ size_t hca_decode_workspace_size(int B, int Hq, int Hkv, int dv) {
 
 namespace {
 
-// hca_decode and hca_decode_vha: the split kernel, then the combine kernel (merge, gate and,
-// with factors, Virtual Head Attention).
 // The split pass (decode.cuh) over a cache, window and workspace whose arguments have been checked; fills in the
 // launch's parameters (p.skip, p.pad and what only the second pass reads are the caller's).
 hca_status_t split_pass(hca::DecodeParams& p, const void* q, const void* kc, const void* vc, const int* page_table,
@@ -423,6 +422,8 @@ hca_status_t split_pass(hca::DecodeParams& p, const void* q, const void* kc, con
     return HCA_OK;
 }
 
+// hca_decode and hca_decode_vha: the split kernel, then the combine kernel (merge, gate and,
+// with factors, Virtual Head Attention).
 hca_status_t decode_impl(const void* q, const void* kc, const void* vc, const int* page_table, int page_size,
                          int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
                          const float* gq, const float* gk, float eps, const void* gate, float* out,
@@ -1044,6 +1045,7 @@ namespace {
 
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool pool_dim(int x) { return x == 64 || x == 128 || x == 256 || x == 512; }
 
 // Checks of a contiguous or paged cache's geometry, shared by the calls below.
@@ -1259,4 +1261,171 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
     mp.B = B; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = p.G; mp.nsplit = nsplit;
     mp.out_f32 = (flags & HCA_OUT_F32) ? 1 : 0;
     return launch_merge(mp, false, s);
+}
+
+// ---------------------------------------------------------------------------------------
+// hca_decode_shared: a batch over one copy of its common prefix (prefix.cuh, decode.cuh, merge.cuh).
+namespace {
+
+// Workspace: the split pass's part, then the prefix records and, for QK normalisation, the normalised queries and
+// the keys' inverse norms.
+struct SharedWs {
+    DecodeWs own;
+    size_t m_off, o_off, q_off, k_off, bytes;
+    long long records;            // prefix records
+    int tpt, tiles, row_tiles, kstride;
+};
+
+// false: a size out of range
+bool shared_ws_layout(SharedWs& w, int B, int Hq, int Hkv, int Np, int nsplit) {
+    const long long U = (long long)B * Hkv;
+    if (U > (1 << 24) || Hq / Hkv > hca::kDecHeads) return false;
+    w.own = decode_ws_layout(U, nsplit);
+    w.tpt = std::min(128 / (Hq / Hkv), B);
+    w.tiles = (int)(((long long)Np + hca::kPpKeys - 1) / hca::kPpKeys);
+    const long long rt = (long long)((B + w.tpt - 1) / w.tpt) * Hkv;
+    w.records = rt + nsplit / 2;
+    if (w.records * 128 > 0x7fffffffLL) return false;
+    w.row_tiles = (int)rt;
+    w.kstride = w.tiles * hca::kPpKeys;
+    w.m_off = align256(w.own.bytes);
+    w.o_off = align256(w.m_off + (size_t)w.records * 128 * sizeof(float));
+    w.q_off = align256(w.o_off + (size_t)w.records * 128 * hca::kDecD * sizeof(float));
+    w.k_off = align256(w.q_off + (size_t)B * Hq * hca::kDecD * 2);
+    w.bytes = align256(w.k_off + (size_t)Hkv * w.kstride * sizeof(float));
+    return true;
+}
+
+template <bool NORM>
+hca_status_t launch_prefix(const hca::PrefixParams& p, int clusters, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const CUtensorMap& tv, const CUtensorMap& tout, cudaStream_t s) {
+    const auto kern = hca::prefix_kernel<NORM>;
+    if (!hca::set_smem_attr_once(reinterpret_cast<const void*>(kern), (int)hca::kPpSmem, 20 + NORM)) return HCA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * (unsigned)clusters);
+    cfg.blockDim = dim3(hca::kPpThreads);
+    cfg.dynamicSmemBytes = hca::kPpSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p, tq, tk, tv, tout) != cudaSuccess) {
+        cudaGetLastError();
+        return HCA_ERR_CUDA;
+    }
+    return HCA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t hca_decode_shared_workspace_size(int B, int Hq, int Hkv, int dv, int Np) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || dv < 1 || Np < 0 || Hq % Hkv) return 0;
+    const int ns = hca::num_sms();
+    SharedWs w;
+    if (ns <= 0 || B == 0 || !shared_ws_layout(w, B, Hq, Hkv, Np, ns)) return 0;
+    return w.bytes;
+}
+
+extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const void* vp, const void* kc, const void* vc,
+                                          const int* page_table, int page_size, int max_pages, int num_pages,
+                                          const void* kw, const void* vw, const int* seqlens, const float* gq,
+                                          const float* gk, float eps, const void* gate, const float* vha_u,
+                                          const float* vha_v, int vha_rank, void* out, void* workspace, size_t ws_bytes,
+                                          int B, int Hq, int Hkv, int d, int dv, int blk, int W, int Np, int Nmax,
+                                          float scale, unsigned flags, hca_stream_t stream) {
+    using namespace hca;
+    if (B < 0 || Hq < 1 || Hkv < 1 || blk < 1 || W < 1 || Np < 0) return HCA_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)(HCA_QK_NORM | HCA_OUT_GATE | HCA_PAGED | HCA_WINDOW_RING | HCA_OUT_F32))
+        return HCA_ERR_UNSUPPORTED;
+    if (d != kDecD || dv != kDecD || Hq % Hkv != 0 || Hq / Hkv > kDecHeads || blk > 128) return HCA_ERR_UNSUPPORTED;
+    if (!(scale == scale) || !(eps >= 0.f)) return HCA_ERR_INVALID_ARG;
+    if (B == 0) return HCA_OK;
+    const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM, gated = flags & HCA_OUT_GATE;
+    if (!q || !kc || !vc || !kw || !vw || !seqlens || !out || !workspace || (Np > 0 && (!kp || !vp)))
+        return HCA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kp) || !aligned16(vp) || !aligned16(kc) || !aligned16(vc) || !aligned16(kw) ||
+        !aligned16(vw) || !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
+        return HCA_ERR_INVALID_ARG;
+    if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    if (norm && (!gq || !gk || !aligned8(gq) || !aligned8(gk))) return HCA_ERR_INVALID_ARG;
+    if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
+    if (vha_u || vha_v) {
+        if (!vha_u || !vha_v || vha_rank < 1 || !aligned4(vha_u) || !aligned4(vha_v)) return HCA_ERR_INVALID_ARG;
+        if (Hkv != 1 || vha_rank > kDecVhaMaxRank) return HCA_ERR_UNSUPPORTED;
+    }
+    const int nsplit = num_sms();
+    if (nsplit <= 0) return HCA_ERR_CUDA;
+    SharedWs lay;
+    if (!shared_ws_layout(lay, B, Hq, Hkv, Np, nsplit) || ws_bytes < lay.bytes) return HCA_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+    // the sequences' own entries and windows
+    DecodeParams dp = {};
+    dp.skip = Np;
+    dp.pad = 1;
+    hca_status_t st = split_pass(dp, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps, ws,
+                                 lay.own, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
+    if (st != HCA_OK) return st;
+
+    MergeParams mp = {};
+    if (Np > 0) {
+        PrefixParams p = {};
+        p.seqlens = seqlens;
+        p.pfx_m = reinterpret_cast<float*>(ws + lay.m_off);
+        p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.tpt = lay.tpt; p.blk = blk; p.W = W; p.Np = Np;
+        p.nct = lay.tiles; p.kstride = lay.kstride;
+        p.scale_log2 = scale * 1.4426950408889634f;
+        p.total = (long long)lay.row_tiles * lay.tiles;
+        p.per = std::max(1LL, (p.total + nsplit / 2 - 1) / (nsplit / 2));
+        const int clusters = (int)((p.total + p.per - 1) / p.per);
+        if (norm) {
+            PrefixPrepParams pp = {};
+            pp.q = static_cast<const __nv_bfloat16*>(q);
+            pp.kp = static_cast<const __nv_bfloat16*>(kp);
+            pp.gq = gq;
+            pp.gk = gk;
+            pp.qn = reinterpret_cast<__nv_bfloat16*>(ws + lay.q_off);
+            pp.kinv = reinterpret_cast<float*>(ws + lay.k_off);
+            pp.nq = (long long)B * Hq;
+            pp.Np = Np; pp.Hkv = Hkv; pp.kstride = lay.kstride; pp.eps = eps;
+            p.kinv = pp.kinv;
+            const long long rows = pp.nq + (long long)Np * Hkv;
+            prefix_prep_kernel<<<(unsigned)((rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, s>>>(pp);
+            if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+        }
+        const uint64_t hd = (uint64_t)Hkv * kDecD;
+        CUtensorMap tq, tk, tv, tout;
+        bool ok = make_tmap_4d(&tq, norm ? static_cast<const void*>(ws + lay.q_off) : q, kDecD, Hq, B, 1, kDecD,
+                               (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, p.G, p.tpt, 1);
+        ok &= make_tmap_4d(&tk, kp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, kPpKeys, 1);
+        ok &= make_tmap_4d(&tv, vp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, 64, 1);
+        const uint64_t rows = (uint64_t)lay.records * 128;
+        ok &= make_tmap_4d_plain(&tout, ws + lay.o_off, 4, kDecD, rows, 1, 1, kDecD, rows * kDecD, rows * kDecD, 32, 32, 1, 1);
+        if (!ok) return HCA_ERR_CUDA;
+        st = norm ? launch_prefix<true>(p, clusters, tq, tk, tv, tout, s) : launch_prefix<false>(p, clusters, tq, tk, tv, tout, s);
+        if (st != HCA_OK) return st;
+        mp.pfx_m = p.pfx_m;
+        mp.pfx_o = reinterpret_cast<const float*>(ws + lay.o_off);
+        mp.tpt = p.tpt;
+        mp.pfx_tiles = p.nct;
+        mp.pfx_per = p.per;
+    }
+    mp.seqlens = seqlens;
+    mp.meta = dp.meta;
+    mp.rec_m = dp.rec_m;
+    mp.rec_l = dp.rec_l;
+    mp.rec_o = dp.rec_o;
+    mp.gate = gated ? static_cast<const __nv_bfloat16*>(gate) : nullptr;
+    mp.vha_u = vha_u;
+    mp.vha_v = vha_v;
+    mp.vha_r = vha_u ? vha_rank : 0;
+    mp.out = out;
+    mp.B = B; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = Hq / Hkv; mp.nsplit = nsplit;
+    mp.out_f32 = (flags & HCA_OUT_F32) ? 1 : 0;
+    return launch_merge(mp, Np > 0, s);
 }

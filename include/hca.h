@@ -423,6 +423,26 @@ hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, con
                               int B, int Hq, int Hkv, int d, int dv, int blk, int W, int Nmax,
                               float scale, unsigned flags, hca_stream_t stream);
 
+/*
+ * hca_decode_shared -- hca_decode of a batch whose sequences all begin with the same Np compressed entries (one
+ * document, many turns), held once: kp, vp [Np,Hkv,512] bf16.  Entry j of a sequence is the prefix's for
+ * j < Np and row j - Np of the sequence's own cache (kc, vc: contiguous [B,Nmax,Hkv,512] or pages) from there on;
+ * visibility goes by seqlens (which count the prefix's tokens) as in hca_decode, so a sequence that is still
+ * inside the prefix sees only the part before its window.  Np == 0 is a batch without a prefix (kp, vp NULL).
+ * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v as for hca_decode_quant; gq, gk 8-byte aligned;
+ * every other argument and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row:
+ * its output is zero.  The workspace: hca_decode_shared_workspace_size bytes.
+ */
+size_t hca_decode_shared_workspace_size(int B, int Hq, int Hkv, int dv, int Np);
+hca_status_t hca_decode_shared(const void* q, const void* kp, const void* vp, const void* kc, const void* vc,
+                               const int* page_table, int page_size, int max_pages, int num_pages,
+                               const void* kw, const void* vw, const int* seqlens,
+                               const float* gq, const float* gk, float eps, const void* gate,
+                               const float* vha_u, const float* vha_v, int vha_rank,
+                               void* out, void* workspace, size_t ws_bytes,
+                               int B, int Hq, int Hkv, int d, int dv, int blk, int W, int Np, int Nmax,
+                               float scale, unsigned flags, hca_stream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char* hca_status_string(hca_status_t status);
 
