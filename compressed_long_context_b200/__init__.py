@@ -10,6 +10,8 @@ article, section "1. Latent-Gated Sparse Attention"): every 128 tokens of K/V ar
 pooled into one cached entry, and each query attends, in one causal softmax, to all
 completed entries plus a window of the W most recent raw tokens.
 """
+import functools
+
 import torch
 
 from . import _lib
@@ -402,59 +404,86 @@ def gate_logits(cq, wg, out=None):
     return out
 
 
-def _scales(t, n, device):
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _all(device, *specs):
+    """_need and _room of several (tensor, dtype, elements, name), in a serving step's time (the calls below take a
+    dozen tensors each and last microseconds on the GPU)."""
+    for t, dtype, n, name in specs:
+        try:
+            good = t.dtype is dtype and t.device == device and t.is_contiguous() and t.numel() >= n
+        except AttributeError:
+            good = False
+        if not good:
+            _need(t, dtype, name, device)
+            _room(t, n, name)
+
+
+def _scale_type(sc):
     """The e8m0 scale pairs of an 8-bit cache: float8_e8m0fnu or uint8."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+    dtype = getattr(sc, "dtype", None)
+    if dtype is not _E8M0 and dtype is not _U8:
         raise TypeError("sc must be a float8_e8m0fnu or uint8 torch.Tensor")
-    _need(t, t.dtype, "sc", device)
-    _room(t, n, "sc")
+    return dtype
 
 
 def _run(name, dev, *args):
     """One call of the library on the tensors' device and its current stream."""
     fn = getattr(_lib.load(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)), name)
+    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+        code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), name)
+            code = fn(*args, _raw_stream(dev))
+    if code:
+        raise HCAError(code, name)
+
+
+def _raw_stream(dev):
+    """_stream without the Stream object around it (2.3 us of a call)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if dev.type == "cuda" else _stream(dev)
+
+
+@functools.lru_cache(maxsize=256)
+def _ws_size(fn, device, *sizes):
+    """A workspace size for these sizes on this device (it depends on the device's SM count)."""
+    with torch.cuda.device(device):
+        return max(fn(*sizes), 1)
 
 
 def _cache_shape(kc, page_table, B, device):
     """(flags, page_size, max_pages, num_pages, Nmax, rows) of a contiguous cache or a page pool."""
     if page_table is None:
-        return 0, 0, 0, 0, kc.shape[1], B * kc.shape[1]
-    _need(page_table, torch.int32, "page_table", device)
+        n = kc.shape[1]
+        return 0, 0, 0, 0, n, B * n
     max_pages = page_table.shape[1]
-    _room(page_table, B * max_pages, "page_table")
-    return HCA_PAGED, kc.shape[1], max_pages, kc.shape[0], 0, kc.shape[0] * kc.shape[1]
+    _all(device, (page_table, _I32, B * max_pages, "page_table"))
+    pages, size = kc.shape[:2]
+    return HCA_PAGED, size, max_pages, pages, 0, pages * size
 
 
 def compress_quant(k, v, w=None, blk=128, kc=None, vc=None, sc=None):
     """``compress`` into the 8-bit form: k [B,T,Hkv,d], v [B,T,Hkv,dv] bf16, w [B,T] fp32 or None.
     Returns (kc, vc, sc): float8_e4m3fn codes [B, T // blk, Hkv, d|dv] and float8_e8m0fnu scales
     [B, T // blk, Hkv, 2] (key, value); an entry's value is code * scale."""
-    _need(k, torch.bfloat16, "k")
+    _need(k, _BF16, "k")
     dev = k.device
-    _need(v, torch.bfloat16, "v", dev)
     B, T, Hkv, d = k.shape
     dv = v.shape[3]
-    if w is not None:
-        _need(w, torch.float32, "w", dev)
-    Nc = T // blk
+    Nc = T // blk if blk > 0 else 0
+    n = B * Nc * Hkv
     if kc is None:
-        kc = torch.empty((B, Nc, Hkv, d), dtype=torch.float8_e4m3fn, device=dev)
+        kc = torch.empty((B, Nc, Hkv, d), dtype=_E4M3, device=dev)
     if vc is None:
-        vc = torch.empty((B, Nc, Hkv, dv), dtype=torch.float8_e4m3fn, device=dev)
+        vc = torch.empty_like(kc) if d == dv else torch.empty((B, Nc, Hkv, dv), dtype=_E4M3, device=dev)
     if sc is None:
-        sc = torch.empty((B, Nc, Hkv, 2), dtype=torch.float8_e8m0fnu, device=dev)
-    _need(kc, torch.float8_e4m3fn, "kc", dev)
-    _need(vc, torch.float8_e4m3fn, "vc", dev)
-    _room(v, B * T * Hkv * dv, "v")
-    _room(w, B * T, "w")
-    _room(kc, B * Nc * Hkv * d, "kc")
-    _room(vc, B * Nc * Hkv * dv, "vc")
-    _scales(sc, B * Nc * Hkv * 2, dev)
+        sc = torch.empty((B, Nc, Hkv, 2), dtype=_E8M0, device=dev)
+    _all(dev, (v, _BF16, B * T * Hkv * dv, "v"), (kc, _E4M3, n * d, "kc"), (vc, _E4M3, n * dv, "vc"),
+         (sc, _scale_type(sc), 2 * n, "sc"))
+    if w is not None:
+        _all(dev, (w, _F32, B * T, "w"))
     _run("hca_compress_quant", dev, _p(k), _p(v), _p(w), _p(kc), _p(vc), _p(sc), B, T, Hkv, d, dv, blk)
     return kc, vc, sc
 
@@ -463,55 +492,78 @@ def append_quant(k_new, v_new, w_new, seqlens, kw, vw, kc, vc, sc, state, blk, p
     """``append`` into an 8-bit cache: the newest token enters the window ring, and a block it completes
     becomes one entry of kc / vc (float8_e4m3fn, contiguous [B,Nmax,Hkv,d|dv] or page pools with
     page_table) and sc (its scales).  Other arguments as for ``append``; seqlens[b] == 0 skips a row."""
-    _need(k_new, torch.bfloat16, "k_new")
+    _need(k_new, _BF16, "k_new")
     dev = k_new.device
-    for name, t in (("v_new", v_new), ("kw", kw), ("vw", vw)):
-        _need(t, torch.bfloat16, name, dev)
-    _need(kc, torch.float8_e4m3fn, "kc", dev)
-    _need(vc, torch.float8_e4m3fn, "vc", dev)
-    _need(seqlens, torch.int32, "seqlens", dev)
-    if w_new is not None:
-        _need(w_new, torch.float32, "w_new", dev)
-    if not isinstance(state, torch.Tensor) or state.dtype not in (torch.uint8, torch.float32):
-        raise TypeError("state must be a uint8 or float32 torch.Tensor")
-    _need(state, state.dtype, "state", dev)
     B, Hkv, d = k_new.shape
     dv, W = v_new.shape[2], kw.shape[1]
-    if state.numel() * state.element_size() < append_state_size(B, Hkv, d, dv):
-        raise ValueError("state is smaller than append_state_size()")
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
-    for name, t, n in (("v_new", v_new, B * Hkv * dv), ("w_new", w_new, B), ("seqlens", seqlens, B),
-                       ("kw", kw, B * W * Hkv * d), ("vw", vw, B * W * Hkv * dv), ("kc", kc, rows * Hkv * d),
-                       ("vc", vc, rows * Hkv * dv)):
-        _room(t, n, name)
-    _scales(sc, rows * Hkv * 2, dev)
+    dtype = getattr(state, "dtype", None)
+    if dtype is not _U8 and dtype is not _F32:
+        raise TypeError("state must be a uint8 or float32 torch.Tensor")
+    words = -(-_state_bytes(B, Hkv, d, dv) // (1 if dtype is _U8 else 4))
+    n = rows * Hkv
+    _all(dev, (v_new, _BF16, B * Hkv * dv, "v_new"), (kw, _BF16, B * W * Hkv * d, "kw"), (vw, _BF16, B * W * Hkv * dv, "vw"),
+         (kc, _E4M3, n * d, "kc"), (vc, _E4M3, n * dv, "vc"), (sc, _scale_type(sc), 2 * n, "sc"), (seqlens, _I32, B, "seqlens"),
+         (state, dtype, words, "state"))
+    if w_new is not None:
+        _all(dev, (w_new, _F32, B, "w_new"))
     _run("hca_append_quant", dev, _p(k_new), _p(v_new), _p(w_new), _p(seqlens), _p(kw), _p(vw), _p(kc), _p(vc), _p(sc),
          _p(page_table), page_size, max_pages, num_pages, _p(state), B, Hkv, d, dv, int(blk), W, Nmax, flags)
+
+
+@functools.lru_cache(maxsize=256)
+def _state_bytes(B, Hkv, d, dv):
+    return append_state_size(B, Hkv, d, dv)
 
 
 def read_quant(kc, vc, sc, counts, n, page_table=None, k_out=None, v_out=None):
     """Entries 0 .. counts[b] - 1 of an 8-bit cache (contiguous, or page pools with page_table) in bf16.
     counts [B] int32.  Returns (k [B,n,Hkv,d], v [B,n,Hkv,dv]); rows at and past counts[b] are left as they
     are (zero in tensors that this call makes)."""
-    _need(kc, torch.float8_e4m3fn, "kc")
+    _need(kc, _E4M3, "kc")
     dev = kc.device
-    _need(vc, torch.float8_e4m3fn, "vc", dev)
-    _need(counts, torch.int32, "counts", dev)
     B, Hkv, d, dv = counts.shape[0], kc.shape[2], kc.shape[3], vc.shape[3]
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
     if k_out is None:
-        k_out = torch.zeros((B, n, Hkv, d), dtype=torch.bfloat16, device=dev)
+        k_out = torch.zeros((B, n, Hkv, d), dtype=_BF16, device=dev)
     if v_out is None:
-        v_out = torch.zeros((B, n, Hkv, dv), dtype=torch.bfloat16, device=dev)
-    _need(k_out, torch.bfloat16, "k_out", dev)
-    _need(v_out, torch.bfloat16, "v_out", dev)
-    for name, t, m in (("kc", kc, rows * Hkv * d), ("vc", vc, rows * Hkv * dv), ("k_out", k_out, B * n * Hkv * d),
-                       ("v_out", v_out, B * n * Hkv * dv)):
-        _room(t, m, name)
-    _scales(sc, rows * Hkv * 2, dev)
+        v_out = torch.zeros((B, n, Hkv, dv), dtype=_BF16, device=dev)
+    m = rows * Hkv
+    _all(dev, (kc, _E4M3, m * d, "kc"), (vc, _E4M3, m * dv, "vc"), (sc, _scale_type(sc), 2 * m, "sc"),
+         (counts, _I32, B, "counts"), (k_out, _BF16, B * n * Hkv * d, "k_out"), (v_out, _BF16, B * n * Hkv * dv, "v_out"))
     _run("hca_read_quant", dev, _p(kc), _p(vc), _p(sc), _p(page_table), page_size, max_pages, num_pages, _p(counts),
          _p(k_out), _p(v_out), B, int(n), Hkv, d, dv, Nmax, flags)
     return k_out, v_out
+
+
+def _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q):
+    """(flags, out, rank) of the arguments that decode_quant and decode_shared have in common."""
+    flags = 0
+    if kw.shape[1] != W or vw.shape[1] != W:
+        raise ValueError("kw and vw must be [B, W, Hkv, 512] with W = %d" % W)
+    if gq is not None or gk is not None:
+        _all(dev, (gq, _F32, d, "gq"), (gk, _F32, d, "gk"))
+        flags |= HCA_QK_NORM
+    if gate is not None:
+        _all(dev, (gate, _BF16, B * Hq * dv, "gate"))
+        flags |= HCA_OUT_GATE
+    if window_ring:
+        flags |= HCA_WINDOW_RING
+    dtype = _BF16
+    if out_f32:
+        flags |= HCA_OUT_F32
+        dtype = _F32
+    if out is None:
+        out = torch.empty_like(q) if d == dv and not out_f32 else torch.empty((B, Hq, dv), dtype=dtype, device=dev)
+    else:
+        _all(dev, (out, dtype, B * Hq * dv, "out"))
+    r = 0
+    if vha_u is not None or vha_v is not None:
+        _all(dev, (vha_u, _F32, 0, "vha_u"), (vha_v, _F32, 0, "vha_v"))
+        r = vha_u.shape[1]
+        if vha_u.shape != (Hq, r) or vha_v.shape != (Hq, r):
+            raise ValueError("vha_u and vha_v must both be [Hq, r]")
+    return flags, out, r
 
 
 def decode_quant(q, kc, vc, sc, kw, vw, seqlens, blk, W, scale, page_table=None, gq=None, gk=None, eps=1e-6,
@@ -519,52 +571,26 @@ def decode_quant(q, kc, vc, sc, kw, vw, seqlens, blk, W, scale, page_table=None,
     """``decode`` over an 8-bit cache: kc / vc float8_e4m3fn and sc (scales), contiguous [B,Nmax,Hkv,..] or
     page pools with page_table; kw / vw the raw bf16 window.  Other arguments as for ``decode``.
     Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero."""
-    _need(q, torch.bfloat16, "q")
+    _need(q, _BF16, "q")
     dev = q.device
-    _need(kc, torch.float8_e4m3fn, "kc", dev)
-    _need(vc, torch.float8_e4m3fn, "vc", dev)
-    _need(kw, torch.bfloat16, "kw", dev)
-    _need(vw, torch.bfloat16, "vw", dev)
-    _need(seqlens, torch.int32, "seqlens", dev)
     B, Hq, d = q.shape
     Hkv, dv = kc.shape[2], vc.shape[3]
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
-    if gq is not None or gk is not None:
-        _need(gq, torch.float32, "gq", dev)
-        _need(gk, torch.float32, "gk", dev)
-        flags |= HCA_QK_NORM
-    if gate is not None:
-        _need(gate, torch.bfloat16, "gate", dev)
-        flags |= HCA_OUT_GATE
-    if window_ring:
-        flags |= HCA_WINDOW_RING
-    if out is None:
-        out = torch.empty((B, Hq, dv), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
-    _need(out, torch.float32 if out_f32 else torch.bfloat16, "out", dev)
-    if out_f32:
-        flags |= HCA_OUT_F32
-    for name, t, n in (("kc", kc, rows * Hkv * d), ("vc", vc, rows * Hkv * dv), ("kw", kw, B * W * Hkv * d),
-                       ("vw", vw, B * W * Hkv * dv), ("seqlens", seqlens, B), ("gq", gq, d), ("gk", gk, d),
-                       ("gate", gate, B * Hq * dv), ("out", out, B * Hq * dv)):
-        _room(t, n, name)
-    _scales(sc, rows * Hkv * 2, dev)
-    r = 0
-    if vha_u is not None or vha_v is not None:
-        _need(vha_u, torch.float32, "vha_u", dev)
-        _need(vha_v, torch.float32, "vha_v", dev)
-        r = vha_u.shape[1]
-        if vha_u.shape != (Hq, r) or vha_v.shape != (Hq, r):
-            raise ValueError("vha_u and vha_v must both be [Hq, r]")
+    n = rows * Hkv
+    _all(dev, (kc, _E4M3, n * d, "kc"), (vc, _E4M3, n * dv, "vc"), (sc, _scale_type(sc), 2 * n, "sc"),
+         (kw, _BF16, B * W * Hkv * d, "kw"), (vw, _BF16, B * W * Hkv * dv, "vw"), (seqlens, _I32, B, "seqlens"))
+    f, out, r = _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q)
     if workspace is None:
-        workspace = torch.empty((max(decode_workspace_size(B, Hq, Hkv, dv), 1),), dtype=torch.uint8, device=dev)
-    _need(workspace, torch.uint8, "workspace", dev)
+        workspace = torch.empty(_ws_size(decode_workspace_size, dev, B, Hq, Hkv, dv), dtype=_U8, device=dev)
+    else:
+        _all(dev, (workspace, _U8, 0, "workspace"))
     _run("hca_decode_quant", dev, _p(q), _p(kc), _p(vc), _p(sc), _p(page_table), page_size, max_pages, num_pages, _p(kw),
          _p(vw), _p(seqlens), _p(gq), _p(gk), float(eps), _p(gate), _p(vha_u), _p(vha_v), r, _p(out), _p(workspace),
-         workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Nmax, float(scale), flags)
+         workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Nmax, float(scale), flags | f)
     return out
 
 
-def decode_shared_workspace_size(B, Hq, Hkv, dv, Np):
+def decode_shared_workspace_size(B, Hq, Hkv, dv, Np) -> int:
     return _lib.load().hca_decode_shared_workspace_size(B, Hq, Hkv, dv, Np)
 
 
@@ -574,44 +600,21 @@ def decode_shared(q, kp, vp, kc, vc, kw, vw, seqlens, blk, W, scale, page_table=
     once for all: kp / vp [Np,Hkv,512] bf16.  kc / vc hold each sequence's entries from the Np-th on (contiguous
     [B,Nmax,Hkv,512], or page pools with page_table); seqlens count the prefix's tokens too.  Other arguments
     as for ``decode``.  Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero."""
-    _need(q, torch.bfloat16, "q")
+    _need(q, _BF16, "q")
     dev = q.device
-    for name, t in (("kp", kp), ("vp", vp), ("kc", kc), ("vc", vc), ("kw", kw), ("vw", vw)):
-        _need(t, torch.bfloat16, name, dev)
-    _need(seqlens, torch.int32, "seqlens", dev)
     B, Hq, d = q.shape
     Np, Hkv, dv = kp.shape[0], kc.shape[2], vc.shape[3]
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
-    if gq is not None or gk is not None:
-        _need(gq, torch.float32, "gq", dev)
-        _need(gk, torch.float32, "gk", dev)
-        flags |= HCA_QK_NORM
-    if gate is not None:
-        _need(gate, torch.bfloat16, "gate", dev)
-        flags |= HCA_OUT_GATE
-    if window_ring:
-        flags |= HCA_WINDOW_RING
-    if out is None:
-        out = torch.empty((B, Hq, dv), dtype=torch.float32 if out_f32 else torch.bfloat16, device=dev)
-    _need(out, torch.float32 if out_f32 else torch.bfloat16, "out", dev)
-    if out_f32:
-        flags |= HCA_OUT_F32
-    for name, t, n in (("kp", kp, Np * Hkv * d), ("vp", vp, Np * Hkv * dv), ("kc", kc, rows * Hkv * d),
-                       ("vc", vc, rows * Hkv * dv), ("kw", kw, B * W * Hkv * d), ("vw", vw, B * W * Hkv * dv),
-                       ("seqlens", seqlens, B), ("gq", gq, d), ("gk", gk, d), ("gate", gate, B * Hq * dv),
-                       ("out", out, B * Hq * dv)):
-        _room(t, n, name)
-    r = 0
-    if vha_u is not None or vha_v is not None:
-        _need(vha_u, torch.float32, "vha_u", dev)
-        _need(vha_v, torch.float32, "vha_v", dev)
-        r = vha_u.shape[1]
-        if vha_u.shape != (Hq, r) or vha_v.shape != (Hq, r):
-            raise ValueError("vha_u and vha_v must both be [Hq, r]")
+    n = rows * Hkv
+    _all(dev, (kp, _BF16, Np * Hkv * d, "kp"), (vp, _BF16, Np * Hkv * dv, "vp"), (kc, _BF16, n * d, "kc"),
+         (vc, _BF16, n * dv, "vc"), (kw, _BF16, B * W * Hkv * d, "kw"), (vw, _BF16, B * W * Hkv * dv, "vw"),
+         (seqlens, _I32, B, "seqlens"))
+    f, out, r = _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q)
     if workspace is None:
-        workspace = torch.empty((max(decode_shared_workspace_size(B, Hq, Hkv, dv, Np), 1),), dtype=torch.uint8, device=dev)
-    _need(workspace, torch.uint8, "workspace", dev)
+        workspace = torch.empty(_ws_size(decode_shared_workspace_size, dev, B, Hq, Hkv, dv, Np), dtype=_U8, device=dev)
+    else:
+        _all(dev, (workspace, _U8, 0, "workspace"))
     _run("hca_decode_shared", dev, _p(q), _p(kp), _p(vp), _p(kc), _p(vc), _p(page_table), page_size, max_pages, num_pages,
          _p(kw), _p(vw), _p(seqlens), _p(gq), _p(gk), float(eps), _p(gate), _p(vha_u), _p(vha_v), r, _p(out), _p(workspace),
-         workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Np, Nmax, float(scale), flags)
+         workspace.numel(), B, Hq, Hkv, d, dv, blk, W, Np, Nmax, float(scale), flags | f)
     return out

@@ -1267,13 +1267,13 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
 // hca_decode_shared: a batch over one copy of its common prefix (prefix.cuh, decode.cuh, merge.cuh).
 namespace {
 
-// Workspace: the split pass's part, then the prefix records and, for QK normalisation, the normalised queries and
-// the keys' inverse norms.
+// Workspace: the split pass's part, then the prefix records and, for QK normalisation, the normalised queries (with
+// their logit scales) and prefix keys.
 struct SharedWs {
     DecodeWs own;
-    size_t m_off, o_off, q_off, k_off, bytes;
+    size_t m_off, o_off, s_off, q_off, k_off, bytes;
     long long records;            // prefix records
-    int tpt, tiles, row_tiles, kstride;
+    int tpt, tiles, row_tiles;
 };
 
 // false: a size out of range
@@ -1283,36 +1283,65 @@ bool shared_ws_layout(SharedWs& w, int B, int Hq, int Hkv, int Np, int nsplit) {
     w.own = decode_ws_layout(U, nsplit);
     w.tpt = std::min(128 / (Hq / Hkv), B);
     w.tiles = (int)(((long long)Np + hca::kPpKeys - 1) / hca::kPpKeys);
-    const long long rt = (long long)((B + w.tpt - 1) / w.tpt) * Hkv;
-    w.records = rt + nsplit / 2;
-    if (w.records * 128 > 0x7fffffffLL) return false;
+    const long long rt = (long long)((B + 2 * w.tpt - 1) / (2 * w.tpt)) * Hkv;
+    w.records = rt + nsplit / 4;
+    if (w.records * 256 > 0x7fffffffLL) return false;
     w.row_tiles = (int)rt;
-    w.kstride = w.tiles * hca::kPpKeys;
     w.m_off = align256(w.own.bytes);
-    w.o_off = align256(w.m_off + (size_t)w.records * 128 * sizeof(float));
-    w.q_off = align256(w.o_off + (size_t)w.records * 128 * hca::kDecD * sizeof(float));
+    w.o_off = align256(w.m_off + (size_t)w.records * 256 * sizeof(float));
+    w.s_off = align256(w.o_off + (size_t)w.records * 256 * hca::kDecD * sizeof(float));
+    w.q_off = align256(w.s_off + (size_t)B * Hq * sizeof(float));
     w.k_off = align256(w.q_off + (size_t)B * Hq * hca::kDecD * 2);
-    w.bytes = align256(w.k_off + (size_t)Hkv * w.kstride * sizeof(float));
+    w.bytes = align256(w.k_off + (size_t)Np * Hkv * hca::kDecD * 2);
     return true;
+}
+
+// The prefix pass's launch over `clusters` clusters of four CTAs (attr: one element, which cfg points to).
+template <bool NORM>
+bool prefix_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters, cudaStream_t s) {
+    if (!hca::set_smem_attr_once(reinterpret_cast<const void*>(hca::prefix_kernel<NORM>), (int)hca::kPpSmem, 20 + NORM))
+        return false;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(4 * (unsigned)clusters);
+    cfg.blockDim = dim3(hca::kPpThreads);
+    cfg.dynamicSmemBytes = hca::kPpSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return true;
+}
+
+// Clusters that can be resident at once on the current device (at most a quarter of its SMs).
+template <bool NORM>
+int prefix_clusters(cudaStream_t s) {
+    static std::mutex mu;
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> g(mu);
+    if (cached[dev] > 0) return cached[dev];
+    const int sms = hca::num_sms();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    int n = 0;
+    if (sms < 4 || !prefix_config<NORM>(cfg, attr, sms / 4, s) ||
+        cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(hca::prefix_kernel<NORM>), &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return cached[dev] = std::min(n, sms / 4);
 }
 
 template <bool NORM>
 hca_status_t launch_prefix(const hca::PrefixParams& p, int clusters, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, const CUtensorMap& tout, cudaStream_t s) {
     const auto kern = hca::prefix_kernel<NORM>;
-    if (!hca::set_smem_attr_once(reinterpret_cast<const void*>(kern), (int)hca::kPpSmem, 20 + NORM)) return HCA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * (unsigned)clusters);
-    cfg.blockDim = dim3(hca::kPpThreads);
-    cfg.dynamicSmemBytes = hca::kPpSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    if (!prefix_config<NORM>(cfg, attr, clusters, s)) return HCA_ERR_CUDA;
     if (cudaLaunchKernelEx(&cfg, kern, p, tq, tk, tv, tout) != cudaSuccess) {
         cudaGetLastError();
         return HCA_ERR_CUDA;
@@ -1378,10 +1407,12 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         p.seqlens = seqlens;
         p.pfx_m = reinterpret_cast<float*>(ws + lay.m_off);
         p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.tpt = lay.tpt; p.blk = blk; p.W = W; p.Np = Np;
-        p.nct = lay.tiles; p.kstride = lay.kstride;
+        p.nct = lay.tiles;
         p.scale_log2 = scale * 1.4426950408889634f;
         p.total = (long long)lay.row_tiles * lay.tiles;
-        p.per = std::max(1LL, (p.total + nsplit / 2 - 1) / (nsplit / 2));
+        const int most = norm ? prefix_clusters<true>(s) : prefix_clusters<false>(s);
+        if (most <= 0) return HCA_ERR_CUDA;
+        p.per = (p.total + most - 1) / most;
         const int clusters = (int)((p.total + p.per - 1) / p.per);
         if (norm) {
             PrefixPrepParams pp = {};
@@ -1389,22 +1420,26 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
             pp.kp = static_cast<const __nv_bfloat16*>(kp);
             pp.gq = gq;
             pp.gk = gk;
-            pp.qn = reinterpret_cast<__nv_bfloat16*>(ws + lay.q_off);
-            pp.kinv = reinterpret_cast<float*>(ws + lay.k_off);
+            pp.qn = reinterpret_cast<__half*>(ws + lay.q_off);
+            pp.kn = reinterpret_cast<__half*>(ws + lay.k_off);
+            pp.qscale = reinterpret_cast<float*>(ws + lay.s_off);
             pp.nq = (long long)B * Hq;
-            pp.Np = Np; pp.Hkv = Hkv; pp.kstride = lay.kstride; pp.eps = eps;
-            p.kinv = pp.kinv;
-            const long long rows = pp.nq + (long long)Np * Hkv;
-            prefix_prep_kernel<<<(unsigned)((rows + kPrepThreads / 32 - 1) / (kPrepThreads / 32)), kPrepThreads, 0, s>>>(pp);
+            pp.nk = (long long)Np * Hkv;
+            pp.eps = eps;
+            pp.scale_log2 = p.scale_log2;
+            p.qscale = pp.qscale;
+            const long long per_cta = kPrepThreads / 32 * kPrepRows;
+            prefix_prep_kernel<<<(unsigned)((pp.nq + pp.nk + per_cta - 1) / per_cta), kPrepThreads, 0, s>>>(pp);
             if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
         }
         const uint64_t hd = (uint64_t)Hkv * kDecD;
         CUtensorMap tq, tk, tv, tout;
         bool ok = make_tmap_4d(&tq, norm ? static_cast<const void*>(ws + lay.q_off) : q, kDecD, Hq, B, 1, kDecD,
                                (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, p.G, p.tpt, 1);
-        ok &= make_tmap_4d(&tk, kp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, kPpKeys, 1);
+        ok &= make_tmap_4d(&tk, norm ? static_cast<const void*>(ws + lay.k_off) : kp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1,
+                           kPpKeys / 2, 1);
         ok &= make_tmap_4d(&tv, vp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, 64, 1);
-        const uint64_t rows = (uint64_t)lay.records * 128;
+        const uint64_t rows = (uint64_t)lay.records * 256;
         ok &= make_tmap_4d_plain(&tout, ws + lay.o_off, 4, kDecD, rows, 1, 1, kDecD, rows * kDecD, rows * kDecD, 32, 32, 1, 1);
         if (!ok) return HCA_ERR_CUDA;
         st = norm ? launch_prefix<true>(p, clusters, tq, tk, tv, tout, s) : launch_prefix<false>(p, clusters, tq, tk, tv, tout, s);

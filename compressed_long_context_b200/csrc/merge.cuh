@@ -4,7 +4,7 @@
 //
 // A record is what one CTA gathered for one unit: per head a reference m (log2 units), the sum l of
 // 2^(z - m) and the 512 sums of 2^(z - m) v.  hca_decode_shared adds a second kind: the shared prefix
-// of 128 / G sequences at once, normalised already (l = 1, m = log2 of the sum of exponentials).
+// of 2 * (128 / G) sequences at once, normalised already (l = 1, m = log2 of the sum of exponentials).
 //
 // Grid (units, 512 / 32), 128 threads: a CTA owns all G heads of one unit for 32 channels, thread =
 // (head, 16 channels), so the mixing across heads stays on chip.  The records of a chunk are all
@@ -21,14 +21,14 @@ struct MergeParams {
     const float* rec_m;           // [R][64]
     const float* rec_l;           // [R][64]
     const float* rec_o;           // [R][64][512]
-    const float* pfx_m;           // [RP][128] prefix records (hca_decode_shared), or null
-    const float* pfx_o;           // [RP][128][512], normalised
+    const float* pfx_m;           // [RP][256] prefix records (hca_decode_shared), or null
+    const float* pfx_o;           // [RP][256][512], normalised
     const __nv_bfloat16* gate;    // [B, Hq, 512] or null
     const float* vha_u;           // [Hq, vha_r] or null
     const float* vha_v;
     void* out;                    // [B, Hq, 512]
     int vha_r, B, Hq, Hkv, G, nsplit, out_f32;
-    // prefix records: row tile rt holds sequences rt * tpt .. + tpt - 1 of one KV head; its key tiles are
+    // prefix records: a row tile holds 2 tpt sequences of one KV head, 128 rows for each tpt of them; its key tiles are
     // numbers [rt * pfx_tiles, (rt + 1) * pfx_tiles) of the list that is cut into ranges of pfx_per tiles
     int tpt, pfx_tiles;
     long long pfx_per;
@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
             fold(0, first, last, (size_t)u, hh, kDecHeads);
         }
         if (kPfx && p.pfx_tiles > 0) {
-            const int rt = (b / p.tpt) * p.Hkv + g;
+            const int rt = (b / (2 * p.tpt)) * p.Hkv + g;
             const int pf = (int)((long long)rt * p.pfx_tiles / p.pfx_per);
             const int pl = (int)(((long long)(rt + 1) * p.pfx_tiles - 1) / p.pfx_per);
-            fold(1, pf, pl, (size_t)rt, (b % p.tpt) * p.G + hh, 128);
+            fold(1, pf, pl, (size_t)rt, (b / p.tpt & 1) * 128 + (b % p.tpt) * p.G + hh, 256);
         }
         const float inv = 1.f / L;
 #pragma unroll

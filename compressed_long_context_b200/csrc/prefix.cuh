@@ -2,17 +2,24 @@
 // (first pass of hca_decode_shared).
 //
 // A common prefix of Np entries is held once.  The 64 heads of one sequence fill half an MMA tile and read every
-// entry; here two sequences' heads (or tpt = 128 / G of them) stand in one tile of 128 rows, and every entry
-// is read from L2 once per row tile instead of from memory once per sequence:
+// entry; here the heads of four sequences (2 tpt with tpt = 128 / G) stand in one tile of 256 rows, and every
+// entry is read from L2 once per row tile instead of from memory once per sequence:
 //   z[r, j] = scale q_r . k_j   over the entries j < min(Np, n_c) that row r's sequence sees,
 // one softmax per row over a range of key tiles, kept as a record (m = log2 sum 2^z, O / l) that merge.cuh joins
 // with the row's own entries and window.
 //
 // The list of (row tile, key tile of 256 entries) pairs, row tile by row tile, is cut into one range per
-// cluster.  A cluster of two SMs shares the work by stage, as prefill_pair.cuh does (S = Q K^T and softmax on
-// the first, O += P V with all 512 value columns in tensor memory on the second) and with its shared-memory
-// layout and barriers.
+// cluster of four SMs, which share the work by stage, as prefill_pair.cuh does, and by rows:
+//   ranks 0, 1 (S pair)  S = Q K^T and softmax: M = 256, N = 256 MMAs of the pair (cta_group::2), each SM with its
+//                        128 rows of Q and of S, and half of every K slab;
+//   ranks 2, 3 (O pair)  O += P V, M = 256, N = 256 value columns, all 512 in tensor memory, each SM with its 128
+//                        rows of P and of O, and half of every V slab; S rank h sends its P to O rank h.
+// Why pairs: one SM's 128 x 256 x 512 products take 4096 cycles and read 256 KB of K or V, 64 bytes a cycle, more
+// than L2 delivers to all SMs at once; the pair halves that.  The first MMA issuer of a pair (the leader) waits
+// for both SMs' copies (they count their bytes on the leader's barrier), and its commits arrive at both.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "prefill_pair.cuh"
 
@@ -20,9 +27,9 @@ namespace hca {
 
 struct PrefixParams {
     const int* seqlens;           // [B]
-    const float* kinv;            // [Hkv][kstride] 1 / rms of the prefix keys (QK normalisation)
-    float* pfx_m;                 // [clusters + row tiles][128]
-    int B, Hq, Hkv, G, tpt, blk, W, Np, nct, kstride;
+    const float* qscale;          // [B * Hq] logit scale (log2) of each row of the normalised queries, or null
+    float* pfx_m;                 // [clusters + row tiles][256]
+    int B, Hq, Hkv, G, tpt, blk, W, Np, nct;
     long long total, per;         // pairs of the list, and of a cluster's range
     float scale_log2;
 };
@@ -41,71 +48,172 @@ __device__ __forceinline__ PfxPiece pfx_piece(const PrefixParams& p, long long x
     it.n = (int)min((long long)(p.nct - it.j0), end - x);
     it.next = x + it.n;
     it.g = it.rt % p.Hkv;
-    it.b0 = it.rt / p.Hkv * p.tpt;
+    it.b0 = it.rt / p.Hkv * (2 * p.tpt);
     return it;
 }
 __device__ __forceinline__ int pfx_keys(const PrefixParams& p, const PfxPiece& it, int j) {
     return min(kPpKeys, p.Np - kPpKeys * (it.j0 + j));
 }
-// Prefix entries visible to row r (= sequence in the tile * G + head); rows without a sequence see none.
-__device__ __forceinline__ int pfx_visible(const PrefixParams& p, const PfxPiece& it, int r) {
-    const int b = it.b0 + r / p.G;
+// Prefix entries visible to row r of an SM's half of the tile (= sequence * G + head); rows without a sequence see none.
+__device__ __forceinline__ int pfx_visible(const PrefixParams& p, const PfxPiece& it, int half, int r) {
+    const int b = it.b0 + half * p.tpt + r / p.G;
     if (r >= p.tpt * p.G || b >= p.B) return 0;
     const long long a = (long long)__ldg(p.seqlens + b) - p.W;
     return a > 0 ? (int)min((long long)p.Np, a / p.blk) : 0;
 }
 
-// QK normalisation: one warp per row.  Rows of q become q / rms(q) * g_q * g_k in bf16 (the keys then need only
-// 1 / rms(k), which goes to kinv).
+// Logit scale (log2) of that row's normalised query.
+__device__ __forceinline__ float pfx_qscale(const PrefixParams& p, const PfxPiece& it, int half, int r) {
+    const int b = it.b0 + half * p.tpt + r / p.G;
+    return r < p.tpt * p.G && b < p.B ? __ldg(p.qscale + (size_t)b * p.Hq + it.g * p.G + r % p.G) : 0.f;
+}
+
+// MMA columns of a tile of nk keys: each SM of the pair holds half of them, in rows of 16
+__device__ __forceinline__ int pfx_cols(int nk) { return (nk + 31) & ~31; }
+
+// QK normalisation: one warp for two rows.  The keys become k / rms(k) and the queries q / rms(q) * g_q * g_k, both in
+// fp16: normalised keys are at most sqrt(512), and a query is scaled by the power of two that puts its largest
+// magnitude into [2^13, 2^14) (undone in its logit scale), so both fit, and are rounded to 11 bits where bf16 has
+// 8 (with bf16 queries the outputs of 8191 entries were 1.7 times further off).
 struct PrefixPrepParams {
     const __nv_bfloat16* q;       // [B * Hq][512]
-    const __nv_bfloat16* kp;      // [Np][Hkv][512]
+    const __nv_bfloat16* kp;      // [Np * Hkv][512]
     const float* gq;
     const float* gk;
-    __nv_bfloat16* qn;            // [B * Hq][512]
-    float* kinv;                  // [Hkv][kstride]
-    long long nq;                 // B * Hq
-    int Np, Hkv, kstride;
-    float eps;
+    __half* qn;                   // [B * Hq][512]
+    __half* kn;                   // [Np * Hkv][512]
+    float* qscale;                // [B * Hq]
+    long long nq, nk;             // rows
+    float eps, scale_log2;
 };
 
 constexpr int kPrepThreads = 256;
+constexpr int kPrepRows = 2;      // rows per warp
 
 __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixPrepParams p) {
     const int lane = threadIdx.x & 31;
-    const long long nk = (long long)p.Np * p.Hkv;
-    const long long i = (long long)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-    if (i >= p.nq + nk) return;
-    const bool isq = i < p.nq;
-    const __nv_bfloat16* src = isq ? p.q + i * kPpD : p.kp + (i - p.nq) * kPpD;
-    uint4 x[2];
-    float ss = 0.f;
+    const long long i0 = ((long long)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5)) * kPrepRows;
+    uint4 x[kPrepRows][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        x[u] = __ldg(reinterpret_cast<const uint4*>(src) + 32 * u + lane);
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ss = fmaf(bf16lo(w[e]), bf16lo(w[e]), fmaf(bf16hi(w[e]), bf16hi(w[e]), ss));
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    const float inv = rsqrtf(ss * (1.f / kPpD) + p.eps);
-    if (!isq) {
-        const long long r = i - p.nq;
-        if (lane == 0) p.kinv[(r % p.Hkv) * p.kstride + r / p.Hkv] = inv;
-        return;
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int c = 8 * (32 * u + lane);
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 a = __ldg(reinterpret_cast<const float2*>(p.gq + c) + e), b = __ldg(reinterpret_cast<const float2*>(p.gk + c) + e);
-            y[e] = pack_bf16x2(bf16lo(w[e]) * (inv * a.x * b.x), bf16hi(w[e]) * (inv * a.y * b.y));
+    for (int k = 0; k < kPrepRows; ++k) {
+        const long long i = i0 + k;
+        if (i < p.nq + p.nk) {
+            const uint4* src = reinterpret_cast<const uint4*>(i < p.nq ? p.q + i * kPpD : p.kp + (i - p.nq) * kPpD);
+            x[k][0] = __ldg(src + lane);
+            x[k][1] = __ldg(src + 32 + lane);
         }
-        reinterpret_cast<uint4*>(p.qn + i * kPpD)[32 * u + lane] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPrepRows; ++k) {
+        const long long i = i0 + k;
+        if (i >= p.nq + p.nk) return;
+        float f[16];
+        float ss = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t w[4] = {x[k][u].x, x[k][u].y, x[k][u].z, x[k][u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[8 * u + 2 * e] = bf16lo(w[e]);
+                f[8 * u + 2 * e + 1] = bf16hi(w[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        float inv = rsqrtf(ss * (1.f / kPpD) + p.eps);
+        __half* dst = p.kn + (i - p.nq) * kPpD;
+        if (i < p.nq) {
+            float am = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const int c = 8 * (32 * u + lane) + e;
+                    const float2 a = __ldg(reinterpret_cast<const float2*>(p.gq + c));
+                    const float2 b = __ldg(reinterpret_cast<const float2*>(p.gk + c));
+                    f[8 * u + e] *= inv * a.x * b.x;
+                    f[8 * u + e + 1] *= inv * a.y * b.y;
+                    am = fmaxf(am, fmaxf(fabsf(f[8 * u + e]), fabsf(f[8 * u + e + 1])));
+                }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
+            // am = y * 2^(b - 127), 1 <= y < 2; factors in [2^-100, 2^100]
+            const int b = min(max((int)(__float_as_uint(am) >> 23), 40), 240);
+            inv = __uint_as_float((uint32_t)(267 - b) << 23);               // 2^(13 - (b - 127))
+            if (lane == 0) p.qscale[i] = p.scale_log2 * __uint_as_float((uint32_t)(b - 13) << 23);
+            dst = p.qn + i * kPpD;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __half2 h = __floats2half2_rn(f[8 * u + 2 * e] * inv, f[8 * u + 2 * e + 1] * inv);
+                y[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            reinterpret_cast<uint4*>(dst)[32 * u + lane] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+    }
+}
+
+// A row's reference moves when a logit exceeds it by this (log2).  P = 2^(z - m) is a floating number, so its
+// relative precision does not depend on m; the bound only keeps sums of P v in range (|v| < 2^80), and is wide
+// because a move costs a second pass over the unit and a rescaling of O (9000 cycles at most, against 6200 for
+// a tile's products): with 2^8 and one key in a hundred 8 times larger, every second unit of 8191 entries moved.
+constexpr float kPxRescale = 32.f;
+constexpr int kPxRing = 6;                        // 16 KB slabs of K, or units of V, in flight per SM
+constexpr uint32_t kPxSlab = 16384;               // K: 128 keys x 64 channels; V: 64 keys x 128 channels
+// barriers: the S pair and the O pair use their own subsets of one numbering (the leaders are ranks 0 and 2)
+enum : int {
+    kPxFull = 0, kPxEmpty = 6,                    // slabs of both SMs landed (leader) / consumed (both)
+    kPxSFull = 12, kPxSEmpty = 14,                // S tile ready (both) / read (leader)
+    kPxPCons = 16,                                // P unit consumed: all four
+    kPxPFull = 20, kPxCorr = 24,                  // P unit landed (each O rank) / checked and rescaled (leader)
+    kPxOFull = 28, kPxOEmpty = 29, kPxDrain = 30,
+    kPxQFull = 32, kPxQEmpty = 40                 // per Q slab: landed (leader) / free (both)
+};
+
+__device__ __forceinline__ uint32_t px_idesc(int N, int b_mn) { return idesc_bf16(256, N, 0, b_mn); }
+// both operands fp16
+__device__ __forceinline__ uint32_t px_idesc_f16(int N) { return idesc_bf16(256, N, 0, 0) & ~((7u << 7) | (7u << 10)); }
+__device__ __forceinline__ void px_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Arrive on the barrier at this offset of every CTA in `mask` when the pair's MMAs issued so far have completed.
+__device__ __forceinline__ void px_commit(uint64_t* bar, uint32_t mask) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "h"((uint16_t)mask) : "memory");
+}
+// Arrival that orders no memory: what it announces is that this warp's tensor-memory loads are done (waited for
+// before).  A release would also wait for the P stores in flight (1300 cycles a tile).
+__device__ __forceinline__ void px_remote_arrive_relaxed(uint32_t rbar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(rbar) : "memory");
+}
+// Load into this CTA's shared memory, counted on a barrier of the pair's leader (a shared::cluster address).
+__device__ __forceinline__ void px_load_4d(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+__device__ __forceinline__ void px_tmem_alloc(uint32_t* dst) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(dst)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void px_tmem_dealloc(uint32_t taddr) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(512) : "memory");
+}
+// A producer that gave up: its copies count on the leader's barrier, which it cannot wait on from here.  They take
+// microseconds; give them a millisecond before this SM's memory is released.
+__device__ __forceinline__ void px_settle() {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
     }
 }
 
@@ -122,38 +230,35 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pp_cluster_rank();
-    const bool s_cta = rank == 0;
+    const bool s_cta = rank < 2;
+    const int half = rank & 1;                    // this SM's 128 rows of the tile
+    const bool leader = half == 0;
     // the swizzled operand tiles need a 1024-byte aligned base; there is no room for slack
     const bool aligned = (smem_u32(dsmem) & 1023u) == 0;
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         misc[2] = aligned ? 1 : 0;
-        for (int i = 0; i < kPpRingK; ++i) {
-            mbar_init(&bars[kBarKFull + i], 1);
-            mbar_init(&bars[kBarKEmpty + i], 1);
-        }
-        for (int i = 0; i < kPpRingV; ++i) {
-            mbar_init(&bars[kBarVFull + i], 1);
-            mbar_init(&bars[kBarVEmpty + i], 1);
+        for (int i = 0; i < kPxRing; ++i) {
+            mbar_init(&bars[kPxFull + i], 1);
+            mbar_init(&bars[kPxEmpty + i], 1);
         }
         for (int i = 0; i < 8; ++i) {
-            mbar_init(&bars[kBarQSFull + i], 1);
-            mbar_init(&bars[kBarQSEmpty + i], 1);
+            mbar_init(&bars[kPxQFull + i], 1);
+            mbar_init(&bars[kPxQEmpty + i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[kBarSFull + i], 1);
-            mbar_init(&bars[kBarSEmpty + i], kPpSoftWarps);
+            mbar_init(&bars[kPxSFull + i], 1);
+            mbar_init(&bars[kPxSEmpty + i], 2 * kPpSoftWarps);
         }
         for (int i = 0; i < kPpSlots; ++i) {
-            mbar_init(&bars[kBarPEmpty + i], 1);
-            mbar_init(&bars[kBarPFull + i], 4);        // armed by each TMEM lane quarter
-            mbar_init(&bars[kBarCorr + i], 4);
-            mbar_init(&bars[kBarPCons + i], 1);
+            mbar_init(&bars[kPxPCons + i], 1);
+            mbar_init(&bars[kPxPFull + i], 4);         // armed by each TMEM lane quarter
+            mbar_init(&bars[kPxCorr + i], 8);
         }
-        mbar_init(&bars[kBarOFull], 1);
-        mbar_init(&bars[kBarOEmpty], 4);
-        mbar_init(&bars[kBarDrain], 1);
+        mbar_init(&bars[kPxOFull], 1);
+        mbar_init(&bars[kPxOEmpty], 8);
+        mbar_init(&bars[kPxDrain], 1);
         fence_mbar_init();
         if (s_cta) {
             prefetch_tmap(&tm_q);
@@ -163,57 +268,59 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             prefetch_tmap(&tm_out);
         }
     }
-    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    if (warp == 1) px_tmem_alloc(tmem_slot);
     tc_fence_before();
     __syncthreads();
-    pp_cluster_sync();      // barriers of both CTAs are initialised before any remote arrive
+    pp_cluster_sync();      // every CTA's barriers are initialised before any remote arrive
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t peer_base = pp_mapa(smem_u32(sm), rank ^ 1u);
-    const bool go = aligned && pp_ld_cluster_u32(peer_base + kPpSmMisc + 8) != 0;
+    const uint32_t peer_base = pp_mapa(smem_u32(sm), rank ^ 2u);          // S rank h <-> O rank h
+    const uint32_t lead_bars = pp_mapa(smem_u32(bars), rank & 2u);        // barriers of the pair's leader
+    const uint32_t pair_mask = s_cta ? 0x3u : 0xcu;
+    bool go = true;
+    for (uint32_t c = 0; c < 4; ++c) go &= pp_ld_cluster_u32(pp_mapa(smem_u32(misc + 2), c)) != 0;
     if (!go && threadIdx.x == 0) record_error(HCA_ERR_INTERNAL);
-    const int cl = blockIdx.x >> 1;               // this cluster's range of the list of (row tile, key tile)
+    const int cl = blockIdx.x >> 2;               // this cluster's range of the list of (row tile, key tile)
     const long long x_beg = cl * p.per, x_end = min(p.total, x_beg + p.per);
 
     if (s_cta && warp == 0) {
-        // ===================================================== S-CTA: TMA of Q and K
+        // ===================================================== S pair: TMA of Q and K
         if (lane == 0 && go) {
             uint32_t kr = 0, qn = 0;
             bool ok = true;
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end)) {
                 for (int j = 0; ok && j < it.n; ++j) {
-                    const int row = (it.j0 + j) * kPpKeys;
+                    // the pair's N = 256 (or the 32-rounded key count) splits evenly over the two SMs
+                    const int row = (it.j0 + j) * kPpKeys + half * (pfx_cols(pfx_keys(p, it, j)) / 2);
                     for (int s = 0; s < 8; ++s) {
                         if (j == 0) {
                             // Q slab s of this row tile, as soon as the previous row tile's last
                             // MMAs on slab s have completed (not after its whole last tile)
-                            if (!mbar_wait(&bars[kBarQSEmpty + s], (qn & 1) ^ 1, abort_flag)) {
+                            if (!pp_wait_cl(&bars[kPxQEmpty + s], (qn & 1) ^ 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
-                            mbar_arrive_expect_tx(&bars[kBarQSFull + s], (uint32_t)(p.tpt * p.G) * 128u);
-                            tma_load_4d(sm + kPpSmQ + s * kPpQSlab, &tm_q, &bars[kBarQSFull + s], 64 * s,
-                                        it.g * p.G, it.b0, 0);
+                            if (leader)
+                                mbar_arrive_expect_tx(&bars[kPxQFull + s], 2u * (uint32_t)(p.tpt * p.G) * 128u);
+                            px_load_4d(sm + kPpSmQ + s * kPpQSlab, &tm_q, lead_bars + (kPxQFull + s) * 8, 64 * s,
+                                       it.g * p.G, it.b0 + half * p.tpt, 0);
                         }
-                        const uint32_t st = kr % kPpRingK;
-                        if (!mbar_wait(&bars[kBarKEmpty + st], ((kr / kPpRingK) & 1) ^ 1, abort_flag)) {
+                        const uint32_t st = kr % kPxRing;
+                        if (!pp_wait_cl(&bars[kPxEmpty + st], ((kr / kPxRing) & 1) ^ 1, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        mbar_arrive_expect_tx(&bars[kBarKFull + st], kPpUnit);
-                        tma_load_4d(sm + kPpSmRing + st * kPpUnit, &tm_k, &bars[kBarKFull + st],
-                                    64 * s, it.g, row, 0);
+                        if (leader) mbar_arrive_expect_tx(&bars[kPxFull + st], 2 * kPxSlab);
+                        px_load_4d(sm + kPpSmRing + st * kPxSlab, &tm_k, lead_bars + (kPxFull + st) * 8, 64 * s, it.g, row, 0);
                         ++kr;
                     }
                 }
                 ++qn;
             }
-            pp_drain_ring(&bars[kBarKFull], kr, kPpRingK);
-            if (qn)
-                for (int s = 0; s < 8; ++s) pp_drain_wait(&bars[kBarQSFull + s], (qn - 1) & 1);
+            if (!ok || *abort_flag) px_settle();
         }
-    } else if (s_cta && warp == 1) {
-        // ===================================================== S-CTA: S = Q K^T
+    } else if (rank == 0 && warp == 1) {
+        // ===================================================== S pair: S = Q K^T
         if (go) {
             uint32_t kr = 0;
             int n = 0, item_n = 0;
@@ -222,51 +329,51 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end), ++item_n) {
                 for (int j = 0; ok && j < it.n; ++j, ++n) {
                     const int sb = n & 1;
-                    if (!warp_wait(&bars[kBarSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                    if (!pp_warp_wait_cl(&bars[kPxSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int N = (pfx_keys(p, it, j) + 15) & ~15;
-                    const uint32_t id = idesc_bf16(128, N, 0, 0);
+                    const int cols = pfx_cols(pfx_keys(p, it, j));
+                    const uint32_t id = NORM ? px_idesc_f16(cols) : px_idesc(cols, 0);
                     const uint32_t dst = tmem + sb * kPpKeys;
                     for (int s = 0; s < 8; ++s) {
-                        const uint32_t st = kr % kPpRingK;
+                        const uint32_t st = kr % kPxRing;
                         // Q slab s of this row tile (landed once per item, used by every tile)
-                        if ((j == 0 && !warp_wait(&bars[kBarQSFull + s], item_n & 1, abort_flag)) ||
-                            !warp_wait(&bars[kBarKFull + st], (kr / kPpRingK) & 1, abort_flag)) {
+                        if ((j == 0 && !warp_wait(&bars[kPxQFull + s], item_n & 1, abort_flag)) ||
+                            !warp_wait(&bars[kPxFull + st], (kr / kPxRing) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         if (lane == 0) {
-                            const uint32_t kb = smem_u32(sm + kPpSmRing + st * kPpUnit);
+                            const uint32_t kb = smem_u32(sm + kPpSmRing + st * kPxSlab);
                             const uint32_t qa = q_base + s * kPpQSlab;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_ss(dst, smem_desc_sw128(qa + kk * 32, 16, 1024),
+                                px_mma(dst, smem_desc_sw128(qa + kk * 32, 16, 1024),
                                        smem_desc_sw128(kb + kk * 32, 16, 1024), id, (s | kk) ? 1u : 0u);
-                            mma_commit(&bars[kBarKEmpty + st]);
+                            px_commit(&bars[kPxEmpty + st], pair_mask);
                             // the row tile's last use of Q slab s: the next row tile's slab s
                             // may land once these MMAs have completed
-                            if (j == it.n - 1) mma_commit(&bars[kBarQSEmpty + s]);
+                            if (j == it.n - 1) px_commit(&bars[kPxQEmpty + s], pair_mask);
                         }
                         __syncwarp();
                         ++kr;
                     }
                     if (!ok) break;
-                    if (lane == 0) mma_commit(&bars[kBarSFull + sb]);
+                    if (lane == 0) px_commit(&bars[kPxSFull + sb], pair_mask);
                     __syncwarp();
                 }
             }
             if (lane == 0) {
-                mma_commit(&bars[kBarDrain]);
-                pp_drain_wait(&bars[kBarDrain], 0);
+                px_commit(&bars[kPxDrain], 1u << rank);
+                pp_drain_wait(&bars[kPxDrain], 0);
             }
             __syncwarp();
         }
     } else if (s_cta && warp >= 2 && warp < 2 + kPpSoftWarps) {
-        // ===================================================== S-CTA: softmax, P to the O-CTA
+        // ===================================================== S pair: softmax, P to the O pair
         // Eight warps: warp w owns the 32 rows of TMEM lane quarter w % 4 and one half of the
         // columns of every unit (hw = 0: the first 64, hw = 1: the last 64).  The two warps of
         // a quarter keep identical per-row references m (they take the same decisions from
@@ -296,26 +403,25 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             };
             const uint32_t rP = peer_base + kPpSmP + (uint32_t)r * 16u;
             const uint32_t rHdr = peer_base + kPpSmHdr;
-            const uint32_t rPFull = peer_base + kPpSmBar + kBarPFull * 8;
-            const float sl2 = p.scale_log2;
+            const uint32_t rPFull = peer_base + kPpSmBar + kPxPFull * 8;
             int n = 0;            // S tiles
             uint32_t un = 0;      // P units
             bool ok = true;
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end)) {
-                const int vis = pfx_visible(p, it, r);        // prefix entries that this row sees
+                const int vis = pfx_visible(p, it, half, r);        // prefix entries that this row sees
+                const float sl2 = NORM ? pfx_qscale(p, it, half, r) : p.scale_log2;
                 float m = -INFINITY, l = 0.f;     // l: this warp's partial row sum
                 for (int j = 0; ok && j < it.n; ++j, ++n) {
                     const int sb = n & 1;
                     const int nk = pfx_keys(p, it, j);
                     const int key0 = (it.j0 + j) * kPpKeys;
                     const int hi = min(nk, vis - key0);           // valid columns of this row: [0, hi)
-                    if (!pair_agree(warp_wait(&bars[kBarSFull + sb], (n >> 1) & 1, abort_flag))) {
+                    if (!pair_agree(pp_warp_wait_cl(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = tmem + lane_off + sb * kPpKeys;
-                    const float* kn = NORM ? p.kinv + (size_t)it.g * p.kstride + key0 : nullptr;   // 1 / rms of the keys
                     const int nu = pp_units(nk);
                     for (int hh = 0; hh < nu; ++hh, ++un) {
                         const int us = (int)(un % kPpSlots);
@@ -341,26 +447,26 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
                                     const int c = c0 + k;
-                                    if (c < hi) tmax = fmaxf(tmax, v[k] * (NORM ? sl2 * kn[c] : sl2));
+                                    if (c < hi) tmax = fmaxf(tmax, v[k] * sl2);
                                 }
                             }
                             float tother;
                             exchange(tmax, &tother);
                             tmax = fmaxf(tmax, tother);
-                            resc = m != -INFINITY && tmax > m + kPfRescale;
+                            resc = m != -INFINITY && tmax > m + kPxRescale;
                             if (resc) {
                                 al = ex2(m - tmax);
                                 l *= al;
                             }
                             if (resc || (m == -INFINITY && tmax > -INFINITY)) m = tmax;
                         }
-                        // the O-CTA's slot us is free once the PV of unit un - kPpSlots has landed
-                        if (!pair_agree(pp_warp_wait_cl(&bars[kBarPEmpty + us], ((un / kPpSlots) & 1) ^ 1,
+                        // slot us of the O rank is free once the PV of unit un - kPpSlots has landed
+                        if (!pair_agree(pp_warp_wait_cl(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1,
                                                         abort_flag))) {
                             ok = false;
                             break;
                         }
-                        // P in bf16 straight into the O-CTA's slot us: keys 8c..8c+7 of the unit,
+                        // P in bf16 straight into slot us of the O rank: keys 8c..8c+7 of the unit,
                         // this row, at chunk c (2 KB per chunk of 8 keys x 128 rows).  Every store
                         // counts its bytes on the slot's barrier; each lane quarter arms it once
                         // it knows how many bytes it stored (a redone unit is stored twice).
@@ -390,8 +496,8 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
                                         for (int e = 0; e < 8; ++e) {
                                             const int c = cb + 2 * e;
-                                            float d0 = fmaf(v[16 * k16 + 2 * e], NORM ? sl2 * kn[c] : sl2, -mref);
-                                            float d1 = fmaf(v[16 * k16 + 2 * e + 1], NORM ? sl2 * kn[c + 1] : sl2, -mref);
+                                            float d0 = fmaf(v[16 * k16 + 2 * e], sl2, -mref);
+                                            float d1 = fmaf(v[16 * k16 + 2 * e + 1], sl2, -mref);
                                             if (kMasked) {
                                                 d0 = c < hi ? d0 : -INFINITY;
                                                 d1 = c + 1 < hi ? d1 : -INFINITY;
@@ -419,7 +525,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             float dother;
                             exchange(dmax, &dother);
                             dmax = fmaxf(dmax, dother);
-                            const bool over = dmax > kPfRescale;
+                            const bool over = dmax > kPxRescale;
                             if (!__any_sync(0xffffffffu, over)) break;
                             if (over) {
                                 al = ex2(-dmax);
@@ -434,7 +540,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             // every TMEM load of this warp from the tile has completed
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars[kBarSEmpty + sb]);
+                            if (lane == 0) px_remote_arrive_relaxed(lead_bars + (kPxSEmpty + sb) * 8);
                         }
                         const bool last = j == it.n - 1 && hh == nu - 1;
                         float lrow = 0.f;
@@ -454,7 +560,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                 pp_remote_arrive_expect_tx(
                                     pbar, (uint32_t)attempts * (uint32_t)(u_end - hh * kPpUKeys) * 64u + 32u * 4u + 4u);
                             }
-                            if (last) p.pfx_m[(size_t)(cl + it.rt) * 128 + r] = m + log2f(lrow);
+                            if (last) p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] = m + log2f(lrow);
                         }
                     }
                 }
@@ -462,7 +568,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
         }
     }
     else if (!s_cta && warp == 0) {
-        // ===================================================== O-CTA: TMA of V
+        // ===================================================== O pair: TMA of V
         if (lane == 0 && go) {
             uint32_t vr = 0;
             bool ok = true;
@@ -474,31 +580,32 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int nv = (pp_unit_keys(nk, hh) + 63) >> 6;
                         for (int h = 0; ok && h < 2; ++h)
                             for (int u = 0; u < nv; ++u) {
-                                const uint32_t st = vr % kPpRingV;
-                                if (!mbar_wait(&bars[kBarVEmpty + st], ((vr / kPpRingV) & 1) ^ 1, abort_flag)) {
+                                const uint32_t st = vr % kPxRing;
+                                if (!pp_wait_cl(&bars[kPxEmpty + st], ((vr / kPxRing) & 1) ^ 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
-                                mbar_arrive_expect_tx(&bars[kBarVFull + st], kPpUnit);
-                                for (int c = 0; c < 4; ++c)
-                                    tma_load_4d(sm + kPpSmVRing + st * kPpUnit + c * kPpVSub, &tm_v,
-                                                &bars[kBarVFull + st], 256 * h + 64 * c, it.g,
-                                                row + kPpUKeys * hh + 64 * u, 0);
+                                if (leader) mbar_arrive_expect_tx(&bars[kPxFull + st], 2 * kPxSlab);
+                                // this SM's half of the 256 value columns
+                                for (int c = 0; c < 2; ++c)
+                                    px_load_4d(sm + kPpSmVRing + st * kPxSlab + c * kPpVSub, &tm_v,
+                                               lead_bars + (kPxFull + st) * 8, 256 * h + 128 * half + 64 * c, it.g,
+                                               row + kPpUKeys * hh + 64 * u, 0);
                                 ++vr;
                             }
                     }
                 }
             }
-            pp_drain_ring(&bars[kBarVFull], vr, kPpRingV);
+            if (!ok || *abort_flag) px_settle();
         }
-    } else if (!s_cta && warp == 1) {
-        // ===================================================== O-CTA: O += P V
+    } else if (rank == 2 && warp == 1) {
+        // ===================================================== O pair: O += P V
         if (go) {
             uint32_t vr = 0, un = 0;
             int item_n = 0;
             bool ok = true;
             const uint32_t p_base = smem_u32(sm + kPpSmP);
-            const uint32_t id = idesc_bf16(128, 256, 0, 1);
+            const uint32_t id = px_idesc(256, 1);
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end), ++item_n) {
                 for (int j = 0; ok && j < it.n; ++j) {
                     const int nk = pfx_keys(p, it, j);
@@ -507,9 +614,9 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int us = (int)(un % kPpSlots);
                         const uint32_t ph = (un / kPpSlots) & 1;
                         const bool first = j == 0 && hh == 0;
-                        if (!pp_warp_wait_cl(&bars[kBarPFull + us], ph, abort_flag) ||
-                            !warp_wait(&bars[kBarCorr + us], ph, abort_flag) ||
-                            (first && !warp_wait(&bars[kBarOEmpty], (item_n & 1) ^ 1, abort_flag))) {
+                        // both SMs' P has landed and their O rows are rescaled
+                        if (!pp_warp_wait_cl(&bars[kPxCorr + us], ph, abort_flag) ||
+                            (first && !pp_warp_wait_cl(&bars[kPxOEmpty], (item_n & 1) ^ 1, abort_flag))) {
                             ok = false;
                             break;
                         }
@@ -519,43 +626,43 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int nv = (nku + 63) >> 6;
                         for (int h = 0; ok && h < 2; ++h)
                             for (int u = 0; u < nv; ++u) {
-                                const uint32_t st = vr % kPpRingV;
-                                if (!warp_wait(&bars[kBarVFull + st], (vr / kPpRingV) & 1, abort_flag)) {
+                                const uint32_t st = vr % kPxRing;
+                                if (!warp_wait(&bars[kPxFull + st], (vr / kPxRing) & 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
                                 tc_fence_after();
                                 if (lane == 0) {
-                                    const uint32_t vb = smem_u32(sm + kPpSmVRing + st * kPpUnit);
+                                    const uint32_t vb = smem_u32(sm + kPpSmVRing + st * kPxSlab);
                                     const uint32_t pa = p_base + us * kPpPBuf + u * 16384;   // 16 keys = 4 KB
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         if (64 * u + 16 * kk < nku)
-                                            mma_ss(tmem + 256 * h, pp_desc_noswz(pa + kk * 4096, 2048, 128),
+                                            px_mma(tmem + 256 * h, pp_desc_noswz(pa + kk * 4096, 2048, 128),
                                                    smem_desc_sw128(vb + kk * 2048, kPpVSub, 1024), id,
                                                    (first && u == 0 && kk == 0) ? 0u : 1u);
-                                    mma_commit(&bars[kBarVEmpty + st]);
+                                    px_commit(&bars[kPxEmpty + st], pair_mask);
                                 }
                                 __syncwarp();
                                 ++vr;
                             }
                         if (!ok) break;
                         if (lane == 0) {
-                            mma_commit(&bars[kBarPCons + us]);
-                            if (j == it.n - 1 && hh == nu - 1) mma_commit(&bars[kBarOFull]);
+                            px_commit(&bars[kPxPCons + us], 0xfu);
+                            if (j == it.n - 1 && hh == nu - 1) px_commit(&bars[kPxOFull], pair_mask);
                         }
                         __syncwarp();
                     }
                 }
             }
             if (lane == 0) {
-                mma_commit(&bars[kBarDrain]);
-                pp_drain_wait(&bars[kBarDrain], 0);
+                px_commit(&bars[kPxDrain], 1u << rank);
+                pp_drain_wait(&bars[kPxDrain], 0);
             }
             __syncwarp();
         }
     } else if (!s_cta && warp >= 2 && warp <= 5) {
-        // ===================================================== O-CTA: rescale, epilogue
+        // ===================================================== O pair: rescale, epilogue
         if (go) {
             const int q4 = warp & 3;
             const int r = q4 * 32 + lane;
@@ -570,7 +677,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                     const int nu = pp_units(nk);
                     for (int hh = 0; hh < nu; ++hh, ++un) {
                         const int us = (int)(un % kPpSlots);
-                        if (!pp_warp_wait_cl(&bars[kBarPFull + us], (un / kPpSlots) & 1, abort_flag)) {
+                        if (!pp_warp_wait_cl(&bars[kPxPFull + us], (un / kPpSlots) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -592,7 +699,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             // a row of this warp moved its reference maximum (never in the first
                             // unit of an item): scale O once the PV of unit un-1 has landed
                             const uint32_t pu = un - 1;
-                            if (!warp_wait(&bars[kBarPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
+                            if (!pp_warp_wait_cl(&bars[kPxPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -613,21 +720,22 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             }
                             tmem_wait_st();
                         }
+                        fence_proxy_async_smem();     // P came through the generic proxy; the pair's MMAs read it
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[kBarCorr + us]);
+                        if (lane == 0) pp_remote_arrive(lead_bars + (kPxCorr + us) * 8);
                     }
                 }
                 if (!ok) break;
                 // ---- epilogue: the record O / l.  Each warp stages 32 rows x 128 bytes at a time in
                 // shared memory and writes them with one TMA tensor store (a coalesced box);
                 // per-lane row stores would touch 32 lines per instruction.
-                if (!warp_wait(&bars[kBarOFull], item_n & 1, abort_flag)) break;
+                if (!pp_warp_wait_cl(&bars[kPxOFull], item_n & 1, abort_flag)) break;
                 tc_fence_after();
                 const float inv = l == 0.f ? 0.f : 1.f / l;       // a row that sees nothing here: zeros
                 uint8_t* stg = sm + kPpSmStage + q4 * kPpStageWarp;
                 const int r0 = q4 * 32;                       // first row of this warp's box
-                const int orow = (cl + it.rt) * 128 + r0;
+                const int orow = (cl + it.rt) * 256 + half * 128 + r0;
 #pragma unroll 1
                 for (int c0 = 0, k = 0; c0 < kPpD; c0 += 32, ++k) {
                     uint8_t* buf = stg + (k & 1) * (kPpStageWarp / 2);
@@ -651,30 +759,10 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                 if (lane == 0) pp_bulk_wait_read0();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kBarOEmpty]);
+                if (lane == 0) pp_remote_arrive(lead_bars + kPxOEmpty * 8);
             }
             if (lane == 0) pp_bulk_wait_all();     // every output store has completed
             __syncwarp();
-        }
-    } else if (!s_cta && warp == 7) {
-        // ===================================================== O-CTA: P slot consumed -> S-CTA
-        if (lane == 0 && go) {
-            const uint32_t rPEmpty = peer_base + kPpSmBar + kBarPEmpty * 8;
-            uint32_t un = 0;
-            bool ok = true;
-            for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end)) {
-                for (int j = 0; ok && j < it.n; ++j) {
-                    const int nu = pp_units(pfx_keys(p, it, j));
-                    for (int hh = 0; hh < nu; ++hh, ++un) {
-                        const int us = (int)(un % kPpSlots);
-                        if (!mbar_wait(&bars[kBarPCons + us], (un / kPpSlots) & 1, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        pp_remote_arrive(rPEmpty + us * 8);
-                    }
-                }
-            }
         }
     }
 
@@ -684,7 +772,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
     pp_cluster_sync();      // no remote store or arrive is still aimed at a CTA that leaves
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        px_tmem_dealloc(tmem);
     }
 }
 
