@@ -1271,7 +1271,7 @@ namespace {
 // their logit scales) and prefix keys.
 struct SharedWs {
     DecodeWs own;
-    size_t m_off, o_off, s_off, q_off, k_off, bytes;
+    size_t m_off, l_off, o_off, s_off, q_off, k_off, bytes;
     long long records;            // prefix records
     int tpt, tiles, row_tiles;
 };
@@ -1288,7 +1288,8 @@ bool shared_ws_layout(SharedWs& w, int B, int Hq, int Hkv, int Np, int nsplit) {
     if (w.records * 256 > 0x7fffffffLL) return false;
     w.row_tiles = (int)rt;
     w.m_off = align256(w.own.bytes);
-    w.o_off = align256(w.m_off + (size_t)w.records * 256 * sizeof(float));
+    w.l_off = align256(w.m_off + (size_t)w.records * 256 * sizeof(float));
+    w.o_off = align256(w.l_off + (size_t)w.records * 256 * sizeof(float));
     w.s_off = align256(w.o_off + (size_t)w.records * 256 * hca::kDecD * sizeof(float));
     w.q_off = align256(w.s_off + (size_t)B * Hq * sizeof(float));
     w.k_off = align256(w.q_off + (size_t)B * Hq * hca::kDecD * 2);
@@ -1406,6 +1407,7 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         PrefixParams p = {};
         p.seqlens = seqlens;
         p.pfx_m = reinterpret_cast<float*>(ws + lay.m_off);
+        p.pfx_l = reinterpret_cast<float*>(ws + lay.l_off);
         p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.tpt = lay.tpt; p.blk = blk; p.W = W; p.Np = Np;
         p.nct = lay.tiles;
         p.scale_log2 = scale * 1.4426950408889634f;
@@ -1445,6 +1447,7 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         st = norm ? launch_prefix<true>(p, clusters, tq, tk, tv, tout, s) : launch_prefix<false>(p, clusters, tq, tk, tv, tout, s);
         if (st != HCA_OK) return st;
         mp.pfx_m = p.pfx_m;
+        mp.pfx_l = p.pfx_l;
         mp.pfx_o = reinterpret_cast<const float*>(ws + lay.o_off);
         mp.tpt = p.tpt;
         mp.pfx_tiles = p.nct;

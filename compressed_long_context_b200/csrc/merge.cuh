@@ -4,7 +4,7 @@
 //
 // A record is what one CTA gathered for one unit: per head a reference m (log2 units), the sum l of
 // 2^(z - m) and the 512 sums of 2^(z - m) v.  hca_decode_shared adds a second kind: the shared prefix
-// of 2 * (128 / G) sequences at once, normalised already (l = 1, m = log2 of the sum of exponentials).
+// of 2 * (128 / G) sequences at once.
 //
 // Grid (units, 512 / 32), 128 threads: a CTA owns all G heads of one unit for 32 channels, thread =
 // (head, 16 channels), so the mixing across heads stays on chip.  The records of a chunk are all
@@ -22,7 +22,8 @@ struct MergeParams {
     const float* rec_l;           // [R][64]
     const float* rec_o;           // [R][64][512]
     const float* pfx_m;           // [RP][256] prefix records (hca_decode_shared), or null
-    const float* pfx_o;           // [RP][256][512], normalised
+    const float* pfx_l;           // [RP][256]
+    const float* pfx_o;           // [RP][256][512]
     const __nv_bfloat16* gate;    // [B, Hq, 512] or null
     const float* vha_u;           // [Hq, vha_r] or null
     const float* vha_v;
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
         // `kind` 0: the unit's own records; 1: the prefix records of its row tile
         auto fold = [&](int kind, int first, int last, size_t rec0, int row, int stride) {
             const float* pm = kind ? p.pfx_m : p.rec_m;
+            const float* pl = kind ? p.pfx_l : p.rec_l;
             const float* po = kind ? p.pfx_o : p.rec_o;
             for (int i0 = first; i0 <= last; i0 += kChunk) {
                 float m[kChunk], l[kChunk];
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
                     const bool ok = live && i0 + k <= last;   // ranges are contiguous: every one has a record
                     const size_t rec = (rec0 + (size_t)(i0 + k)) * stride + row;
                     m[k] = ok ? __ldcg(pm + rec) : -INFINITY;
-                    l[k] = kind ? 1.f : (ok ? __ldcg(p.rec_l + rec) : 0.f);
+                    l[k] = ok ? __ldcg(pl + rec) : 0.f;
                     const float4* op = reinterpret_cast<const float4*>(po + rec * kDecD + c);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[k][j] = ok ? __ldcg(op + j) : make_float4(0.f, 0.f, 0.f, 0.f);

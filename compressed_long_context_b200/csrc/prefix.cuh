@@ -5,8 +5,8 @@
 // entry; here the heads of four sequences (2 tpt with tpt = 128 / G) stand in one tile of 256 rows, and every
 // entry is read from L2 once per row tile instead of from memory once per sequence:
 //   z[r, j] = scale q_r . k_j   over the entries j < min(Np, n_c) that row r's sequence sees,
-// one softmax per row over a range of key tiles, kept as a record (m = log2 sum 2^z, O / l) that merge.cuh joins
-// with the row's own entries and window.
+// one softmax per row over a range of key tiles, kept as a record (reference m, l = sum 2^(z - m), O = sum 2^(z - m) v)
+// that merge.cuh joins with those of the row's own entries and window.
 //
 // The list of (row tile, key tile of 256 entries) pairs, row tile by row tile, is cut into one range per
 // cluster of four SMs, which share the work by stage, as prefill_pair.cuh does, and by rows:
@@ -28,7 +28,8 @@ namespace hca {
 struct PrefixParams {
     const int* seqlens;           // [B]
     const float* qscale;          // [B * Hq] logit scale (log2) of each row of the normalised queries, or null
-    float* pfx_m;                 // [clusters + row tiles][256]
+    float* pfx_m;                 // [clusters + row tiles][256] references
+    float* pfx_l;                 // sums of 2^(z - m)
     int B, Hq, Hkv, G, tpt, blk, W, Np, nct;
     long long total, per;         // pairs of the list, and of a cluster's range
     float scale_log2;
@@ -257,7 +258,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             mbar_init(&bars[kPxCorr + i], 8);
         }
         mbar_init(&bars[kPxOFull], 1);
-        mbar_init(&bars[kPxOEmpty], 8);
+        mbar_init(&bars[kPxOEmpty], 16);
         mbar_init(&bars[kPxDrain], 1);
         fence_mbar_init();
         if (s_cta) {
@@ -296,7 +297,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (j == 0) {
                             // Q slab s of this row tile, as soon as the previous row tile's last
                             // MMAs on slab s have completed (not after its whole last tile)
-                            if (!pp_wait_cl(&bars[kPxQEmpty + s], (qn & 1) ^ 1, abort_flag)) {
+                            if (!mbar_wait(&bars[kPxQEmpty + s], (qn & 1) ^ 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -306,7 +307,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                        it.g * p.G, it.b0 + half * p.tpt, 0);
                         }
                         const uint32_t st = kr % kPxRing;
-                        if (!pp_wait_cl(&bars[kPxEmpty + st], ((kr / kPxRing) & 1) ^ 1, abort_flag)) {
+                        if (!mbar_wait(&bars[kPxEmpty + st], ((kr / kPxRing) & 1) ^ 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -329,7 +330,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end), ++item_n) {
                 for (int j = 0; ok && j < it.n; ++j, ++n) {
                     const int sb = n & 1;
-                    if (!pp_warp_wait_cl(&bars[kPxSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                    if (!warp_wait(&bars[kPxSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -346,7 +347,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             break;
                         }
                         tc_fence_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             const uint32_t kb = smem_u32(sm + kPpSmRing + st * kPxSlab);
                             const uint32_t qa = q_base + s * kPpQSlab;
 #pragma unroll
@@ -362,11 +363,11 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         ++kr;
                     }
                     if (!ok) break;
-                    if (lane == 0) px_commit(&bars[kPxSFull + sb], pair_mask);
+                    if (elect_one()) px_commit(&bars[kPxSFull + sb], pair_mask);
                     __syncwarp();
                 }
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 px_commit(&bars[kPxDrain], 1u << rank);
                 pp_drain_wait(&bars[kPxDrain], 0);
             }
@@ -377,7 +378,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
         // Eight warps: warp w owns the 32 rows of TMEM lane quarter w % 4 and one half of the
         // columns of every unit (hw = 0: the first 64, hw = 1: the last 64).  The two warps of
         // a quarter keep identical per-row references m (they take the same decisions from
-        // the same exchanged maxima) and their own partial row sums.
+        // the same exchanged maxima).
         if (go) {
             const int q4 = warp & 3;
             const int hw = (warp - 2) >> 2;
@@ -392,13 +393,13 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                 *other = xch[(xpar * 2 + (hw ^ 1)) * 128 + r];
                 xpar ^= 1;
             };
-            // the two warps of a quarter go on or unwind together: a verdict that differed
+            // a condition of either warp of a quarter, which go on or unwind together: a verdict that differed
             // would leave one of them at a named barrier the other never reaches
-            auto pair_agree = [&](bool ok_mine) -> bool {
+            auto pair_any = [&](bool mine) -> bool {
                 uint32_t res;
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                             "barrier.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                             : "=r"(res) : "r"((uint32_t)ok_mine), "r"(4 + q4) : "memory");
+                             "barrier.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(res) : "r"((uint32_t)mine), "r"(4 + q4) : "memory");
                 return res != 0;
             };
             const uint32_t rP = peer_base + kPpSmP + (uint32_t)r * 16u;
@@ -410,16 +411,13 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end)) {
                 const int vis = pfx_visible(p, it, half, r);        // prefix entries that this row sees
                 const float sl2 = NORM ? pfx_qscale(p, it, half, r) : p.scale_log2;
-                float m = -INFINITY, l = 0.f;     // l: this warp's partial row sum
+                float m = -INFINITY;
                 for (int j = 0; ok && j < it.n; ++j, ++n) {
                     const int sb = n & 1;
                     const int nk = pfx_keys(p, it, j);
                     const int key0 = (it.j0 + j) * kPpKeys;
                     const int hi = min(nk, vis - key0);           // valid columns of this row: [0, hi)
-                    if (!pair_agree(pp_warp_wait_cl(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
+                    const bool live = warp_wait(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag);   // agreed on below
                     tc_fence_after();
                     const uint32_t sa = tmem + lane_off + sb * kPpKeys;
                     const int nu = pp_units(nk);
@@ -430,7 +428,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int c_end = min(c_beg + 64, u_end);             // (may be empty)
                         // The reference maximum m of a row is lazy: P = 2^(logit - m) is computed
                         // against the reference of the earlier units, and m moves only when a unit
-                        // exceeds it by 2^8 -- the unit is then redone against the new reference.
+                        // exceeds it by kPxRescale -- the unit is then redone against the new reference.
                         // A quarter in which some row has no reference yet takes the maximum first.
                         const bool need_max = __any_sync(0xffffffffu, m == -INFINITY && hi > hh * kPpUKeys);
                         bool resc = false;
@@ -438,34 +436,24 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (need_max) {
                             float tmax = -INFINITY;
 #pragma unroll 1
-                            for (int c0 = c_beg; c0 < c_end; c0 += 32) {
-                                float v[32];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-                                    if (c0 + 16 * k < c_end) tmem_ld16(sa + c0 + 16 * k, v + 16 * k);
+                            for (int c0 = c_beg; live && c0 < c_end; c0 += 16) {
+                                float v[16];
+                                tmem_ld16(sa + c0, v);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) {
-                                    const int c = c0 + k;
-                                    if (c < hi) tmax = fmaxf(tmax, v[k] * sl2);
-                                }
+                                for (int k = 0; k < 16; ++k)
+                                    if (c0 + k < hi) tmax = fmaxf(tmax, v[k] * sl2);
                             }
                             float tother;
                             exchange(tmax, &tother);
                             tmax = fmaxf(tmax, tother);
                             resc = m != -INFINITY && tmax > m + kPxRescale;
-                            if (resc) {
-                                al = ex2(m - tmax);
-                                l *= al;
-                            }
+                            if (resc) al = ex2(m - tmax);
                             if (resc || (m == -INFINITY && tmax > -INFINITY)) m = tmax;
                         }
-                        // slot us of the O rank is free once the PV of unit un - kPpSlots has landed
-                        if (!pair_agree(pp_warp_wait_cl(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1,
-                                                        abort_flag))) {
-                            ok = false;
-                            break;
-                        }
+                        // slot us of the O rank is free once the PV of unit un - kPpSlots has landed (a wait that
+                        // ran out is agreed on below: the unit's stores are dropped, its barrier is not armed)
+                        const bool slot = live && warp_wait(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1, abort_flag);
                         // P in bf16 straight into slot us of the O rank: keys 8c..8c+7 of the unit,
                         // this row, at chunk c (2 KB per chunk of 8 keys x 128 rows).  Every store
                         // counts its bytes on the slot's barrier; each lane quarter arms it once
@@ -476,78 +464,77 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         // columns valid for every row of the warp (most compressed units) skip
                         // the per-column mask
                         const bool unmasked = __all_sync(0xffffffffu, hi >= c_end);
-                        float rs, dmax;
-                        auto pass2 = [&](auto masked_tag, float mref) {
+                        float dmax;
+                        // 16 columns from cb: probabilities against mref, stored
+                        auto put16 = [&](auto masked_tag, const float* v, int cb, float2 sl, float2 nm) {
                             constexpr bool kMasked = decltype(masked_tag)::value;
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float2 d = fma2(make_float2(v[2 * e], v[2 * e + 1]), sl, nm);
+                                if (kMasked) {
+                                    d.x = cb + 2 * e < hi ? d.x : -INFINITY;
+                                    d.y = cb + 2 * e + 1 < hi ? d.y : -INFINITY;
+                                }
+                                dmax = max3(dmax, d.x, d.y);
+                                pk[e] = pack_bf16x2(ex2(d.x), ex2(d.y));
+                            }
+                            const uint32_t ra = pbase + ((uint32_t)(cb - hh * kPpUKeys) >> 3) * 2048u;
+                            pp_st_async_v4(ra, pk[0], pk[1], pk[2], pk[3], pbar);
+                            pp_st_async_v4(ra + 2048u, pk[4], pk[5], pk[6], pk[7], pbar);
+                        };
+                        auto pass2 = [&](float mref) {
+                            const float2 sl = make_float2(sl2, sl2), nm = make_float2(-mref, -mref);
                             dmax = -INFINITY;
-                            rs = 0.f;
+                            if (unmasked && c_end == c_beg + 64) {
+                                // the second half's load runs while the first half is worked on
+                                float v[32], w[32];
+                                tmem_ld32(sa + c_beg, v);
+                                tmem_wait_ld32(v);
+                                tmem_ld32(sa + c_beg + 32, w);
+                                put16(std::false_type{}, v, c_beg, sl, nm);
+                                put16(std::false_type{}, v + 16, c_beg + 16, sl, nm);
+                                tmem_wait_ld32(w);
+                                put16(std::false_type{}, w, c_beg + 32, sl, nm);
+                                put16(std::false_type{}, w + 16, c_beg + 48, sl, nm);
+                            } else {
 #pragma unroll 1
-                            for (int c0 = c_beg; c0 < c_end; c0 += 32) {
-                                float v[32];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-                                    if (c0 + 16 * k < c_end) tmem_ld16(sa + c0 + 16 * k, v + 16 * k);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k16 = 0; k16 < 2; ++k16) {
-                                    const int cb = c0 + 16 * k16;
-                                    if (cb < c_end) {
-                                        uint32_t pk[8];
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) {
-                                            const int c = cb + 2 * e;
-                                            float d0 = fmaf(v[16 * k16 + 2 * e], sl2, -mref);
-                                            float d1 = fmaf(v[16 * k16 + 2 * e + 1], sl2, -mref);
-                                            if (kMasked) {
-                                                d0 = c < hi ? d0 : -INFINITY;
-                                                d1 = c + 1 < hi ? d1 : -INFINITY;
-                                            }
-                                            dmax = fmaxf(dmax, fmaxf(d0, d1));
-                                            const float a = ex2(d0), b2 = ex2(d1);
-                                            rs += a + b2;
-                                            pk[e] = pack_bf16x2(a, b2);
-                                        }
-                                        const uint32_t ra = pbase + ((uint32_t)(cb - hh * kPpUKeys) >> 3) * 2048u;
-                                        pp_st_async_v4(ra, pk[0], pk[1], pk[2], pk[3], pbar);
-                                        pp_st_async_v4(ra + 2048u, pk[4], pk[5], pk[6], pk[7], pbar);
-                                    }
+                                for (int c0 = c_beg; c0 < c_end; c0 += 16) {
+                                    float v[16];
+                                    tmem_ld16(sa + c0, v);
+                                    tmem_wait_ld();
+                                    put16(std::true_type{}, v, c0, sl, nm);
                                 }
                             }
                         };
                         for (int attempt = 0;; ++attempt) {
-                            const float mref = m == -INFINITY ? 0.f : m;
-                            if (unmasked)
-                                pass2(std::false_type{}, mref);
-                            else
-                                pass2(std::true_type{}, mref);
-                            if (need_max || attempt) break;
-                            // every row has a reference here; redo if a unit exceeded it
-                            float dother;
-                            exchange(dmax, &dother);
-                            dmax = fmaxf(dmax, dother);
-                            const bool over = dmax > kPxRescale;
-                            if (!__any_sync(0xffffffffu, over)) break;
-                            if (over) {
-                                al = ex2(-dmax);
-                                l *= al;
-                                m += dmax;
+                            if (slot) pass2(m == -INFINITY ? 0.f : m);
+                            // one barrier per pass: a row over its reference, or a wait that ran out?
+                            const bool over = slot && !need_max && !attempt && dmax > kPxRescale;
+                            const float mine = slot ? (over ? dmax : -INFINITY) : NAN;
+                            xch[(xpar * 2 + hw) * 128 + r] = mine;
+                            if (!pair_any(over || !slot)) break;
+                            const float other = xch[(xpar * 2 + (hw ^ 1)) * 128 + r];
+                            xpar ^= 1;
+                            if (__any_sync(0xffffffffu, mine != mine || other != other)) {
+                                ok = false;
+                                break;
+                            }
+                            const float dm = fmaxf(mine, other);
+                            if (!__any_sync(0xffffffffu, dm > kPxRescale)) break;
+                            if (dm > kPxRescale) {
+                                al = ex2(-dm);
+                                m += dm;
                                 resc = true;
                             }
                             attempts = 2;
                         }
-                        l += rs;
+                        if (!ok) break;
                         if (hh == nu - 1) {
                             // every TMEM load of this warp from the tile has completed
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) px_remote_arrive_relaxed(lead_bars + (kPxSEmpty + sb) * 8);
-                        }
-                        const bool last = j == it.n - 1 && hh == nu - 1;
-                        float lrow = 0.f;
-                        if (last) {      // whole-row sums for the epilogue and the LSE
-                            float lother;
-                            exchange(l, &lother);
-                            lrow = l + lother;
                         }
                         if (hw == 0) {
                             // unit header: rescale factor per row, per-quarter flag; then the arm:
@@ -560,7 +547,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                 pp_remote_arrive_expect_tx(
                                     pbar, (uint32_t)attempts * (uint32_t)(u_end - hh * kPpUKeys) * 64u + 32u * 4u + 4u);
                             }
-                            if (last) p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] = m + log2f(lrow);
+                            if (j == it.n - 1 && hh == nu - 1) p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] = m;
                         }
                     }
                 }
@@ -581,7 +568,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         for (int h = 0; ok && h < 2; ++h)
                             for (int u = 0; u < nv; ++u) {
                                 const uint32_t st = vr % kPxRing;
-                                if (!pp_wait_cl(&bars[kPxEmpty + st], ((vr / kPxRing) & 1) ^ 1, abort_flag)) {
+                                if (!mbar_wait(&bars[kPxEmpty + st], ((vr / kPxRing) & 1) ^ 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
@@ -614,13 +601,13 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int us = (int)(un % kPpSlots);
                         const uint32_t ph = (un / kPpSlots) & 1;
                         const bool first = j == 0 && hh == 0;
-                        // both SMs' P has landed and their O rows are rescaled
-                        if (!pp_warp_wait_cl(&bars[kPxCorr + us], ph, abort_flag) ||
-                            (first && !pp_warp_wait_cl(&bars[kPxOEmpty], (item_n & 1) ^ 1, abort_flag))) {
+                        // both SMs' P has landed (seen, and handed to the async proxy, by their rescale warps) and
+                        // their O rows are rescaled
+                        if (!warp_wait(&bars[kPxCorr + us], ph, abort_flag) ||
+                            (first && !warp_wait(&bars[kPxOEmpty], (item_n & 1) ^ 1, abort_flag))) {
                             ok = false;
                             break;
                         }
-                        fence_proxy_async_smem();    // P arrived through the generic proxy
                         tc_fence_after();
                         const int nku = pp_unit_keys(nk, hh);
                         const int nv = (nku + 63) >> 6;
@@ -632,7 +619,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                     break;
                                 }
                                 tc_fence_after();
-                                if (lane == 0) {
+                                if (elect_one()) {
                                     const uint32_t vb = smem_u32(sm + kPpSmVRing + st * kPxSlab);
                                     const uint32_t pa = p_base + us * kPpPBuf + u * 16384;   // 16 keys = 4 KB
 #pragma unroll
@@ -647,7 +634,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                 ++vr;
                             }
                         if (!ok) break;
-                        if (lane == 0) {
+                        if (elect_one()) {
                             px_commit(&bars[kPxPCons + us], 0xfu);
                             if (j == it.n - 1 && hh == nu - 1) px_commit(&bars[kPxOFull], pair_mask);
                         }
@@ -655,24 +642,33 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                     }
                 }
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 px_commit(&bars[kPxDrain], 1u << rank);
                 pp_drain_wait(&bars[kPxDrain], 0);
             }
             __syncwarp();
         }
-    } else if (!s_cta && warp >= 2 && warp <= 5) {
-        // ===================================================== O pair: rescale, epilogue
+    } else if (!s_cta && warp >= 2) {
+        // ===================================================== O pair: rescale (warps 2-5), epilogue (2-9)
         if (go) {
             const int q4 = warp & 3;
+            const bool extra = warp > 5;            // shares the quarter's epilogue only
             const int r = q4 * 32 + lane;
             const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
             uint32_t un = 0;
             int item_n = 0;
             bool ok = true;
+            // a quarter's two warps go on or unwind together
+            auto pair_agree_o = [&](bool ok_mine) -> bool {
+                uint32_t res;
+                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                             "barrier.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                             : "=r"(res) : "r"((uint32_t)ok_mine), "r"(8 + q4) : "memory");
+                return res != 0;
+            };
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end), ++item_n) {
                 float l = 0.f;            // row sum of the bf16 P this CTA multiplies with
-                for (int j = 0; ok && j < it.n; ++j) {
+                for (int j = 0; !extra && ok && j < it.n; ++j) {
                     const int nk = pfx_keys(p, it, j);
                     const int nu = pp_units(nk);
                     for (int hh = 0; hh < nu; ++hh, ++un) {
@@ -699,7 +695,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             // a row of this warp moved its reference maximum (never in the first
                             // unit of an item): scale O once the PV of unit un-1 has landed
                             const uint32_t pu = un - 1;
-                            if (!pp_warp_wait_cl(&bars[kPxPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
+                            if (!warp_wait(&bars[kPxPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -726,33 +722,32 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (lane == 0) pp_remote_arrive(lead_bars + (kPxCorr + us) * 8);
                     }
                 }
-                if (!ok) break;
-                // ---- epilogue: the record O / l.  Each warp stages 32 rows x 128 bytes at a time in
+                if (!pair_agree_o(ok)) break;
+                // ---- epilogue: the record (l, O), half of the columns for each of a quarter's two warps.  Each warp stages 32 rows x 128 bytes at a time in
                 // shared memory and writes them with one TMA tensor store (a coalesced box);
                 // per-lane row stores would touch 32 lines per instruction.
-                if (!pp_warp_wait_cl(&bars[kPxOFull], item_n & 1, abort_flag)) break;
+                if (!pair_agree_o(warp_wait(&bars[kPxOFull], item_n & 1, abort_flag))) break;
                 tc_fence_after();
-                const float inv = l == 0.f ? 0.f : 1.f / l;       // a row that sees nothing here: zeros
-                uint8_t* stg = sm + kPpSmStage + q4 * kPpStageWarp;
+                if (!extra) p.pfx_l[(size_t)(cl + it.rt) * 256 + half * 128 + r] = l;
+                uint8_t* stg = sm + kPpSmStage + (q4 * 2 + extra) * (kPpStageWarp / 2);
                 const int r0 = q4 * 32;                       // first row of this warp's box
                 const int orow = (cl + it.rt) * 256 + half * 128 + r0;
 #pragma unroll 1
-                for (int c0 = 0, k = 0; c0 < kPpD; c0 += 32, ++k) {
-                    uint8_t* buf = stg + (k & 1) * (kPpStageWarp / 2);
-                    if (k >= 2 && lane == 0) pp_bulk_wait_read1();     // the store of piece k-2 read it
-                    __syncwarp();
+                for (int c0 = extra * (kPpD / 2), k = 0; k < kPpD / 64; c0 += 32, ++k) {
                     float o[32];
                     tmem_ld16(tmem + lane_off + c0, o);
                     tmem_ld16(tmem + lane_off + c0 + 16, o + 16);
                     tmem_wait_ld();
+                    if (lane == 0) pp_bulk_wait_read0();              // the previous piece's store has read it
+                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)       // 128-byte swizzle: chunk e of row lane
-                        *reinterpret_cast<float4*>(buf + lane * 128 + (((e ^ lane) & 7) << 4)) =
-                            make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+                        *reinterpret_cast<float4*>(stg + lane * 128 + (((e ^ lane) & 7) << 4)) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        pp_tma_store_4d(&tm_out, buf, c0, orow, 0, 0);
+                        pp_tma_store_4d(&tm_out, stg, c0, orow, 0, 0);
                         pp_bulk_commit();
                     }
                 }
