@@ -101,8 +101,6 @@ struct DecodeParams {
     const float* vha_v;
     int vha_r;
     int B, Hq, Hkv, G, blk, W, Nmax, page_size, max_pages, num_pages, flags, nsplit;
-    int skip;                    // the cache holds the entries from this one on (0: all)
-    int pad;                     // length 0 marks a padding row (else it is an error)
     float scale_log2, eps;
 };
 
@@ -117,12 +115,11 @@ __device__ __forceinline__ UnitTiles unit_tiles(const DecodeParams& p, int u, bo
     t.g = u - t.b * p.Hkv;
     int L = __ldg(p.seqlens + t.b);
     if (L < 1) {
-        if (report && !(p.pad && L == 0)) record_error(HCA_ERR_DEVICE_INPUT);
+        if (report) record_error(HCA_ERR_DEVICE_INPUT);
         L = 1;
     }
     const long long a = (long long)L - p.W;          // (t - W + 1) with t = L - 1
-    const long long nc0 = a > 0 ? a / p.blk : 0;
-    long long nc = nc0 > p.skip ? nc0 - p.skip : 0;
+    long long nc = a > 0 ? a / p.blk : 0;
     const long long cap = (p.flags & HCA_PAGED) ? (long long)p.max_pages * p.page_size : (long long)p.Nmax;
     if (nc > cap) {
         if (report) record_error(HCA_ERR_DEVICE_INPUT);

@@ -20,13 +20,20 @@
 // maximum of y, and the row sum l adds 2^(y - m) / vscale = 2^(z - m).  m is kept 2^6 below the maximum
 // and moves when some y exceeds it by 2^8, so that p <= 256 and 2^6 for the largest key: e4m3 ends at 448.
 //
+// The same kernel with bf16 entries (E8 = false) attends what the sequences of hca_decode_shared do not have in
+// common: then all tiles are of the window's kind, and the reference moves at 2^32 (bf16 holds any p).
+//
 // Inside a CTA (12 warps: a thirteenth would leave 128 registers per thread instead of 168):
-//   warp 0, 3   TMA of K / of V: slabs of 16 KB (128 keys x 128 codes, or x 64 bf16 channels of the window)
-//               through a ring of four each; a tile of entries fills a ring once, a window tile twice;
-//   warp 1      TMA of the query rows, once per (unit, kind of tile): 8-bit hi / lo for entries (made in place
-//               by the softmax warps), bf16 for the window;  tcgen05.mma  S^T[128 keys x 64 heads] = K Q^T;
-//   warp 2      tcgen05.mma  O^T[512 x 64] += V^T P^T;
+//   warp 0, 3   TMA of K / of V: slabs of 16 KB (128 keys x 128 codes, or x 64 bf16 channels) through a ring of
+//               four each; a tile of codes fills a ring once, a bf16 tile twice;
+//   warp 1      TMA of the query rows, once per (unit, kind of tile): 8-bit hi / lo for codes (made in place by
+//               the softmax warps), bf16 otherwise;  tcgen05.mma  S^T[128 keys x 64 heads] = K Q^T;
+//   warp 2      the CTA's range of tiles, then tcgen05.mma  O^T[512 x 64] += V^T P^T over the 32-key (bf16: 16-key)
+//               steps that hold a key;
 //   warps 4-11  softmax, two per TMEM lane quarter, thread = (key row, 32 heads); record at a piece's end.
+// What bounds a small call is its chain of first steps, whose code is fetched cold (about 30 cycles an
+// instruction): they are loops, not unrolled, the range is found by one warp, and the MMA issuers are elected.
+// One 4K sequence (one tile of each kind on two CTAs): 27 -> see the figures at the end of this comment.
 #pragma once
 
 #include "decode.cuh"
@@ -68,17 +75,23 @@ struct QuantParams {
     float* rec_l;
     float* rec_o;
     int B, Hq, Hkv, G, blk, W, Nmax, page_size, max_pages, num_pages, flags, nsplit;
+    int cap;                       // entries that a sequence's cache can hold
+    int skip;                      // the cache holds the entries from this one on (0: all)
+    // hca_decode_shared: this pass runs beside the prefix pass on the SMs that it leaves (0: alone on all)
+    long long pfx_total;
+    int pfx_max;
+    SharedPlan* plan;              // written for the merge
     float scale_log2, eps;
 };
 
 // A unit's tiles: nct tiles of 128 entries (cost 1 each), then nwt tiles of 128 raw window tokens (cost
-// 2: twice the bytes).
+// wc: 2 beside codes, which have half the bytes, else 1).
 struct QUnit {
     int b, g, nc, nw, nct, nwt, s0;
-    __device__ int tiles() const { return nct + nwt; }
-    __device__ int cost() const { return nct + 2 * nwt; }
+    __device__ __forceinline__ int tiles() const { return nct + nwt; }
+    template <int WC> __device__ __forceinline__ int cost() const { return nct + WC * nwt; }
     // first tile that starts at or after cost position x
-    __device__ int tile_at(int x) const { return x <= nct ? x : nct + (x - nct + 1) / 2; }
+    template <int WC> __device__ __forceinline__ int tile_at(int x) const { return x <= nct ? x : nct + (x - nct + WC - 1) / WC; }
 };
 
 __device__ __forceinline__ QUnit q_unit(const QuantParams& p, int u, bool report) {
@@ -90,14 +103,14 @@ __device__ __forceinline__ QUnit q_unit(const QuantParams& p, int u, bool report
         if (report && L < 0) record_error(HCA_ERR_DEVICE_INPUT);
         L = 1;
     }
-    const long long a = (long long)L - p.W;          // (t - W + 1) with t = L - 1
-    long long nc = a > 0 ? a / p.blk : 0;
-    const long long cap = (p.flags & HCA_PAGED) ? (long long)p.max_pages * p.page_size : (long long)p.Nmax;
-    if (nc > cap) {
+    const int a = L - p.W;                           // (t - W + 1) with t = L - 1
+    int nc = (a > 0 ? (int)((unsigned)a / (unsigned)p.blk) : 0) - p.skip;
+    nc = nc > 0 ? nc : 0;
+    if (nc > p.cap) {
         if (report) record_error(HCA_ERR_DEVICE_INPUT);
-        nc = cap;
+        nc = p.cap;
     }
-    t.nc = (int)nc;
+    t.nc = nc;
     t.nw = L < p.W ? L : p.W;
     t.nct = (t.nc + kDecTile - 1) / kDecTile;
     t.nwt = (t.nw + kDecTile - 1) / kDecTile;
@@ -105,63 +118,165 @@ __device__ __forceinline__ QUnit q_unit(const QuantParams& p, int u, bool report
     return t;
 }
 
-// Block-wide inclusive scan of one int per thread (all threads of the CTA call it).
-__device__ __forceinline__ int q_scan(int v, int* warp_tot, int* total_out) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += n;
-    }
-    if (lane == 31) warp_tot[warp] = v;
-    __syncthreads();
-    int pre = 0, tot = 0;
-    for (int w = 0; w < kQdThreads / 32; ++w) {
-        if (w < warp) pre += warp_tot[w];
-        tot += warp_tot[w];
-    }
-    __syncthreads();
-    *total_out = tot;
-    return v + pre;
+// A CTA's range: either tiles [beg, end) of unit u (`aligned`), or the tiles that start in the cost range [beg, end) of
+// the batch's list, in which unit u starts at pu.
+struct QRange {
+    long long beg, end, pu;
+    int u, aligned;
+};
+
+template <typename T>
+__device__ __forceinline__ T q_warp_sum(T v) {
+#pragma unroll 1
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
 }
 
-// This CTA's tiles in order.  Either one unit's tiles [a, b) (`fixed`), or the tiles that start in the
-// cost range [cs, ce) of the batch's list.
+// Found by one warp.  Two ways to cut the batch, as in decode.cuh:
+//  - unit-aligned, when the batch has no more units than CTAs: unit u gets k_u CTAs, k_u between 1 and its tile count,
+//    for the smallest cost per CTA T in tpc .. tpc + 3 whose counts fit the grid; every CTA then holds one piece
+//    (one query load, one record);
+//  - otherwise equal cost ranges of at least the cost of a window tile, so that every CTA between a unit's first
+//    and last holds one of its tiles and leaves a record.
+template <int WC>
+__device__ __noinline__ void q_range(const QuantParams& p, int cta, int grid, QRange* out) {
+    const int lane = threadIdx.x & 31;
+    const int U = p.B * p.Hkv;
+    long long total = 0;
+#pragma unroll 1
+    for (int u = lane; u < U; u += 32) total += q_unit(p, u, true).cost<WC>();
+    total = q_warp_sum(total);
+    int nsplit = p.nsplit;
+    if (p.pfx_total > 0) {
+        const SharedPlan plan = shared_plan_warp(p.pfx_total, total, p.pfx_max, p.nsplit);
+        nsplit = min(plan.splits, grid);
+        if (lane == 0 && cta == 0) *p.plan = plan;
+    }
+    const long long tpc = max((long long)WC, (total + nsplit - 1) / nsplit);
+    QRange r = {min(total, tpc * cta), min(total, tpc * (cta + 1)), 0, -1, 0};
+    int T = 0;
+    if (U <= nsplit && nsplit < 0x4000 && total <= 0x3fffffffll) {
+        // the four candidate counts are summed in one reduction, as 16-bit fields: k_u <= nsplit * cost_u / total + 2
+        // (fl rounds in fp32: one more), so each sum is at most nsplit + 3 U < 2^16
+        const float share = (float)nsplit / (float)total;
+        auto count = [&](const QUnit& t, int w) {
+            const unsigned c = t.cost<WC>(), Tw = (unsigned)tpc + w;
+            return max(1, min(t.tiles(), max((int)((float)c * share), (int)((c + Tw - 1u) / Tw))));
+        };
+        unsigned long long sum = 0;
+#pragma unroll 1
+        for (int u = lane; u < U; u += 32) {
+            const QUnit t = q_unit(p, u, false);
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) sum += (unsigned long long)count(t, w) << (16 * w);
+        }
+        sum = q_warp_sum(sum);
+        int w = 0;
+        while (w < 4 && (int)((sum >> (16 * w)) & 0xffffu) > nsplit) ++w;
+        if (w < 4) {
+            T = 1;
+            int base = 0;
+            r.beg = r.end = 0;
+#pragma unroll 1
+            for (int u0 = 0; u0 < U && base <= cta; u0 += 32) {
+                const int u = u0 + lane;
+                QUnit t = {};
+                int k = 0;
+                if (u < U) {
+                    t = q_unit(p, u, false);
+                    k = count(t, w);
+                }
+                int incl = k;
+#pragma unroll 1
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int n = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += n;
+                }
+                const int i = cta - (base + incl - k);
+                const bool mine = i >= 0 && i < k;
+                if (mine) {
+                    const int c = t.cost<WC>(), n = t.tiles();
+                    r.u = u;
+                    if (WC * k <= c) {                  // every cost range holds a tile's start
+                        r.beg = t.tile_at<WC>((int)((long long)c * i / k));
+                        r.end = t.tile_at<WC>((int)((long long)c * (i + 1) / k));
+                    } else {                            // near one tile per CTA: even tile counts
+                        r.beg = n * i / k;
+                        r.end = n * (i + 1) / k;
+                    }
+                    r.aligned = 1;
+                    *out = r;
+                }
+                if (__any_sync(0xffffffffu, mine)) return;
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+    }
+    if (!T && r.beg < r.end) {
+        // the unit holding cost position beg
+        long long base = 0;
+#pragma unroll 1
+        for (int u0 = 0; u0 < U; u0 += 32) {
+            const int u = u0 + lane;
+            const int c = u < U ? q_unit(p, u, false).cost<WC>() : 0;
+            int incl = c;
+#pragma unroll 1
+            for (int off = 1; off < 32; off <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += n;
+            }
+            const long long pu = base + incl - c;
+            const bool mine = pu <= r.beg && r.beg < pu + c;
+            if (mine) {
+                r.u = u;
+                r.pu = pu;
+                *out = r;
+            }
+            if (__any_sync(0xffffffffu, mine)) return;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    if (lane == 0) *out = r;                            // nothing to do
+}
+
+// This CTA's tiles in order.
+template <bool E8>
 struct QIter {
+    static constexpr int WC = E8 ? 2 : 1;
     const QuantParams* p;
     long long ce, pu;              // end of the range; cost position where unit u starts
     QUnit t;
-    int u, tb, tend, tile, item, qitem;
+    int u, tb, tend, tile, item;
     bool fixed, done;
 
     __device__ void load(long long from) {
         t = q_unit(*p, u, false);
-        tb = t.tile_at((int)((from > pu ? from : pu) - pu));
-        const long long end = pu + t.cost();
-        tend = t.tile_at((int)((ce < end ? ce : end) - pu));
+        tb = t.template tile_at<WC>((int)((from > pu ? from : pu) - pu));
+        const long long end = pu + t.template cost<WC>();
+        tend = t.template tile_at<WC>((int)((ce < end ? ce : end) - pu));
         tile = tb;
     }
-    __device__ void init(const QuantParams* pp, int u0, long long p0, long long a, long long b, bool fix) {
+    __device__ __forceinline__ void init(const QuantParams* pp, const QRange& r) {
         p = pp;
-        u = u0;
-        pu = p0;
-        ce = b;
-        fixed = fix;
-        item = qitem = 0;
-        done = u0 < 0 || a >= b;
+        u = r.u;
+        pu = r.pu;
+        ce = r.end;
+        fixed = r.aligned;
+        item = 0;
+        done = r.u < 0 || r.beg >= r.end;
         if (done) return;
         if (fixed) {
             t = q_unit(*p, u, false);
-            tb = tile = (int)a;
-            tend = (int)b;
+            tb = tile = (int)r.beg;
+            tend = (int)r.end;
         } else {
-            load(a);
+            load(r.beg);
             if (tb >= tend) advance();
         }
     }
-    __device__ void advance() {            // to the next unit with a tile in the range
+    __device__ __forceinline__ void advance() {            // to the next unit with a tile in the range
         do {
-            pu += t.cost();
+            pu += t.template cost<WC>();
             ++u;
             if (fixed || pu >= ce) {
                 done = true;
@@ -173,14 +288,14 @@ struct QIter {
     __device__ bool first() const { return tile == tb; }
     __device__ bool last() const { return tile == tend - 1; }
     __device__ bool comp() const { return tile < t.nct; }
+    __device__ bool codes() const { return E8 && tile < t.nct; }
     // the query rows are loaded for the first tile of each kind in a piece, and free after its last
-    __device__ bool qfirst() const { return tile == tb || tile == t.nct; }
-    __device__ bool qlast() const { return tile == tend - 1 || tile == t.nct - 1; }
+    __device__ bool qfirst() const { return tile == tb || (E8 && tile == t.nct); }
+    __device__ bool qlast() const { return tile == tend - 1 || (E8 && tile == t.nct - 1); }
     __device__ int nvalid() const {
         return comp() ? min(kDecTile, t.nc - tile * kDecTile) : min(kDecTile, t.nw - (tile - t.nct) * kDecTile);
     }
     __device__ void next() {
-        if (qlast()) ++qitem;
         if (++tile < tend) return;
         ++item;
         advance();
@@ -197,7 +312,7 @@ __device__ __forceinline__ int q_page(const QuantParams& p, int b, int j, bool r
     return pg;
 }
 
-template <bool NORM, bool PAGED>
+template <bool NORM, bool PAGED, bool E8>
 __global__ void __launch_bounds__(kQdThreads, 1)
 decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -214,7 +329,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
     uint64_t* full_v = empty_k + kQdRing;
     uint64_t* empty_v = full_v + kQdRing;
     uint64_t* q_tma = empty_v + kQdRing;           // query rows landed
-    uint64_t* q_full = q_tma + 1;                  // query operand ready
+    uint64_t* q_full = q_tma + 1;                  // query operand made from them
     uint64_t* q_empty = q_full + 1;                // query operand no longer read
     uint64_t* s_full = q_empty + 1;                // [kQdLook]
     uint64_t* s_empty = s_full + kQdLook;          // [kQdLook]
@@ -229,155 +344,45 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
     int* misc = reinterpret_cast<int*>(sm + kQsMisc);
     volatile int* abort_flag = misc + 0;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
-    int* sched = misc + 2;                         // [0] first unit, [1] aligned, [2 ..] scan scratch
+    QRange* range = reinterpret_cast<QRange*>(misc + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int U = p.B * p.Hkv;
     const int cta = blockIdx.x;
+    // bf16 probabilities hold any range: the reference starts at the maximum and moves late
+    constexpr float shift = E8 ? kQdShift : 0.f, thr = E8 ? kRescaleThreshold : 32.f;
 
-    if (threadIdx.x == 0) {
+    if (warp == 2) {
+        q_range<E8 ? 2 : 1>(p, cta, gridDim.x, range);
+    } else if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+    } else if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < kQdRing; ++i) {
-            mbar_init(&full_k[i], 1);
-            mbar_init(&empty_k[i], 1);
-            mbar_init(&full_v[i], 1);
-            mbar_init(&empty_v[i], 1);
+        // barriers in order: full / empty of K, of V; q_tma, q_full, q_empty; s_full; s_empty; p_full; p_empty; o_full, o_empty
+#pragma unroll 1
+        for (int i = 0; i < kQdBars; ++i) {
+            const int j = i - 4 * kQdRing;
+            const bool many = j == 1 || (j >= 3 + kQdLook && j < 3 + 2 * kQdLook + kDecPBufs) || i == kQdBars - 1;
+            mbar_init(&full_k[i], many ? kDecSoftWarps : 1);
         }
-        mbar_init(q_tma, 1);
-        mbar_init(q_full, kDecSoftWarps);
-        mbar_init(q_empty, 1);
-        for (int i = 0; i < kQdLook; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_empty[i], kDecSoftWarps);
-        }
-        for (int i = 0; i < kDecPBufs; ++i) {
-            mbar_init(&p_full[i], kDecSoftWarps);
-            mbar_init(&p_empty[i], 1);
-        }
-        mbar_init(o_full, 1);
-        mbar_init(o_empty, kDecSoftWarps);
         fence_mbar_init();
-    }
-    if (warp == 1) tmem_alloc(tmem_slot, 512);
-    if (threadIdx.x == 32) {
+    } else if (threadIdx.x == 96) {
         prefetch_tmap(&tm_q);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_kw);
         prefetch_tmap(&tm_vw);
     }
-
-    // ---- this CTA's tiles.  Two ways to cut the batch, as in decode.cuh:
-    //  - unit-aligned, when the batch has no more units than CTAs: unit u gets k_u CTAs, k_u between
-    //    1 and its tile count, for the smallest cost per CTA T in tpc .. tpc + 3 whose counts fit the
-    //    grid; every CTA then holds one piece (one query load, one record);
-    //  - otherwise equal cost ranges of at least 2 (the cost of one window tile), so that every CTA between
-    //    a unit's first and last holds one of its tiles and leaves a record.
-    const bool small_batch = U <= kQdThreads;
-    int my_c = 0, my_t = 0;
-    long long total = 0;
-    for (int u = threadIdx.x; u < U; u += kQdThreads) {
-        const QUnit t = q_unit(p, u, true);
-        my_c = t.cost();
-        my_t = t.tiles();
-        total += my_c;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    {
-        long long* wt = reinterpret_cast<long long*>(red);
-        if (lane == 0) wt[warp] = total;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < kQdThreads / 32; ++w) total += wt[w];
-        __syncthreads();
-    }
-    const long long tpc = max(2ll, (total + p.nsplit - 1) / p.nsplit);
-    long long* sched64 = reinterpret_cast<long long*>(red + 64);   // [0] start, [1] end, [2] first unit's position
-    unsigned long long* wsum = reinterpret_cast<unsigned long long*>(red);   // [warp]
-    int my_k = 0;
-    bool aligned = false;
-    if (small_batch && U <= p.nsplit && p.nsplit < 0x4000 && total <= 0x3fffffffll) {
-        // the four candidate counts are summed in one reduction, as 16-bit fields: k_u <= nsplit *
-        // cost_u / total + 2, so each sum is at most nsplit + 2 U < 2^16
-        const bool mine = threadIdx.x < U;
-        const unsigned fl = mine ? (unsigned)((long long)my_c * p.nsplit / total) : 0u;
-        unsigned long long packed = 0;
-        if (mine)
-#pragma unroll 1
-            for (unsigned w = 0; w < 4; ++w) {
-                const unsigned T = (unsigned)tpc + w;
-                const unsigned k = min((unsigned)my_t, max(fl, ((unsigned)my_c + T - 1u) / T));
-                packed |= (unsigned long long)max(1u, k) << (16 * w);
-            }
-        unsigned long long sum = packed;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) wsum[warp] = sum;
-        __syncthreads();
-        sum = 0;
-        for (int v = 0; v < kQdThreads / 32; ++v) sum += wsum[v];
-        __syncthreads();
-        for (int w = 3; w >= 0; --w)
-            if ((int)((sum >> (16 * w)) & 0xffffu) <= p.nsplit) {
-                aligned = true;
-                my_k = (int)((packed >> (16 * w)) & 0xffffu);
-            }
-    }
-    if (threadIdx.x == 0) {
-        sched[0] = -1;
-        sched64[0] = aligned ? 0 : min(total, tpc * cta);
-        sched64[1] = aligned ? 0 : min(total, tpc * (cta + 1));
-    }
-    __syncthreads();
-    if (aligned) {
-        int tot;
-        const int incl = q_scan(my_k, sched + 2, &tot);
-        const int cu = incl - my_k;
-        if (threadIdx.x < U && cu <= cta && cta < cu + my_k) {
-            const QUnit t = q_unit(p, threadIdx.x, false);
-            const int i = cta - cu;
-            sched[0] = threadIdx.x;
-            sched64[2] = 0;
-            if (2 * my_k <= my_c) {                // every cost range holds a tile's start
-                sched64[0] = t.tile_at((int)((long long)my_c * i / my_k));
-                sched64[1] = t.tile_at((int)((long long)my_c * (i + 1) / my_k));
-            } else {                               // near one tile per CTA: even tile counts
-                sched64[0] = (long long)my_t * i / my_k;
-                sched64[1] = (long long)my_t * (i + 1) / my_k;
-            }
-        }
-    } else {
-        // the unit holding cost position cs (block-wide scan over units)
-        const long long cs = sched64[0];
-        long long base = 0;
-        for (int c0 = 0; c0 < U; c0 += kQdThreads) {
-            const int u = c0 + threadIdx.x;
-            const int n = u < U ? q_unit(p, u, false).cost() : 0;
-            int tot;
-            const int incl = q_scan(n, sched + 2, &tot);
-            const long long pu = base + incl - n;
-            if (u < U && pu <= cs && cs < pu + n) {
-                sched[0] = u;
-                sched64[2] = pu;
-            }
-            base += tot;
-        }
-    }
-    __syncthreads();
-    const long long r_beg = sched64[0], r_end = sched64[1], p_first = sched64[2];
-    const int u_first = sched[0];
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     constexpr int look = NORM ? kQdLookNorm : kQdLook;
-    QIter it;
-    it.init(&p, u_first, p_first, r_beg, r_end, aligned);
+    QIter<E8> it;
+    it.init(&p, *range);
 
     if (warp == 0 || warp == 3) {
         // ===================================================== TMA of K (warp 0) or V (warp 3), one thread
-        if (lane == 0) {
+        if (elect_one()) {
             const bool is_v = warp == 3;
             uint64_t* full = is_v ? full_v : full_k;
             uint64_t* empty = is_v ? empty_v : empty_k;
@@ -385,73 +390,77 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             const CUtensorMap* mc = is_v ? &tm_v : &tm_k;
             const CUtensorMap* mw = is_v ? &tm_vw : &tm_kw;
             // test switch (hca_debug_set_drop_slab): the first K slab is never requested
-            bool drop = !is_v && *reinterpret_cast<volatile int*>(&g_debug_drop_slab) != 0;
+            const bool drop = !is_v && *reinterpret_cast<volatile int*>(&g_debug_drop_slab) != 0;
             uint32_t n = 0;
             bool ok = true;
             for (; ok && !it.done; it.next()) {
-                const bool comp = it.comp();
+                const bool comp = it.comp(), halves = PAGED && comp;
                 int pg[2] = {0, 0};
                 const int j0 = it.tile * kDecTile;
                 const bool h1 = j0 + 64 < it.t.nc;
-                if (PAGED && comp) {
+                if (halves) {
                     pg[0] = q_page(p, it.t.b, j0, true);
                     pg[1] = h1 ? q_page(p, it.t.b, j0 + 64, true) : pg[0];
                 }
-                const int ns = comp ? 4 : 8;
+                const int ns = it.codes() ? 4 : 8, wide = it.codes() ? 128 : 64;
+                const int row = comp ? j0 : it.t.s0 + (it.tile - it.t.nct) * kDecTile;
+#pragma unroll 1
                 for (int s = 0; s < ns; ++s, ++n) {
                     const uint32_t st = n % kQdRing;
-                    if (!mbar_wait(&empty[st], ((n / kQdRing) & 1) ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (drop) {          // the slab never lands: its consumer's wait runs out
-                        ok = false;
+                    if (!mbar_wait(&empty[st], ((n / kQdRing) & 1) ^ 1, abort_flag) || drop) {   // dropped: its
+                        ok = false;                                                  // consumer's wait runs out
                         break;
                     }
                     uint8_t* dst = ring + st * kSlabBytes;
-                    if (PAGED && comp) {
-                        mbar_arrive_expect_tx(&full[st], h1 ? 2 * 8192 : 8192);
-                        for (int h = 0; h < (h1 ? 2 : 1); ++h)
-                            tma_load_4d(dst + h * 8192, mc, &full[st], 128 * s, it.t.g, (j0 + 64 * h) % p.page_size, pg[h]);
+                    mbar_arrive_expect_tx(&full[st], halves && !h1 ? kSlabBytes / 2 : kSlabBytes);
+                    if (halves) {
+                        tma_load_4d(dst, mc, &full[st], wide * s, it.t.g, j0 % p.page_size, pg[0]);
+                        if (h1) tma_load_4d(dst + 8192, mc, &full[st], wide * s, it.t.g, (j0 + 64) % p.page_size, pg[1]);
                     } else {
-                        mbar_arrive_expect_tx(&full[st], kSlabBytes);
-                        tma_load_4d(dst, comp ? mc : mw, &full[st], (comp ? 128 : 64) * s, it.t.g,
-                                    comp ? j0 : it.t.s0 + (it.tile - it.t.nct) * kDecTile, it.t.b);
+                        tma_load_4d(dst, comp ? mc : mw, &full[st], wide * s, it.t.g, row, it.t.b);
                     }
                 }
             }
             mbar_drain_ring(full, n, kQdRing);
         }
+        __syncwarp();
     } else if (warp == 1) {
-        // ===================================================== QK^T issuer (warp waits, lane 0 issues)
+        // ===================================================== QK^T issuer (warp waits, one lane issues)
         const uint32_t id_w = idesc_bf16(128, kDecHeads, 0, 0), id_wkk = idesc_bf16(128, 128, 0, 0);
         const uint32_t id_e = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE4M3, 0, 0);
         const uint32_t id_ekk = idesc_f8(128, 128, kFmtE4M3, kFmtE4M3, 0, 0);
         const uint32_t q_base = smem_u32(sm + kQsQ);
-        uint32_t ks = 0, nq = 0;
+        uint32_t ks = 0, nq = 0, nconv = 0;
         for (int n = 0; !it.done; it.next(), ++n) {
             const int sb = n % look;
+            const bool codes = it.codes();
             if (it.qfirst()) {
                 // the query rows of the piece (or its window part), once this warp's MMAs no longer read
                 // the ones before
                 if (!warp_wait(q_empty, (nq & 1) ^ 1, abort_flag)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_arrive_expect_tx(q_tma, kDecQBytes);
+#pragma unroll 1
                     for (int s = 0; s < kDecSlabs; ++s)
                         tma_load_4d(sm + kQsQ + s * 8192, &tm_q, q_tma, 64 * s, it.t.g * p.G, it.t.b, 0);
                 }
                 __syncwarp();
                 ++nq;
-                if (!warp_wait(q_full, it.qitem & 1, abort_flag)) break;
+                if (NORM || codes) {
+                    if (!warp_wait(q_full, nconv & 1, abort_flag)) break;
+                    ++nconv;
+                } else if (!warp_wait(q_tma, (nq - 1) & 1, abort_flag)) {
+                    break;
+                }
             }
             if (!warp_wait(&s_empty[sb], ((n / look) & 1) ^ 1, abort_flag)) break;
             // the K K^T accumulator has one buffer: wait until tile n-1's softmax has read it
             if (NORM && n > 0 && !warp_wait(&s_empty[(n - 1) % look], ((n - 1) / look) & 1, abort_flag)) break;
             tc_fence_after();
             const uint32_t dst = tmem + dec_s_col(sb);
-            const bool comp = it.comp();
-            const int ns = comp ? 4 : 8;
+            const int ns = codes ? 4 : 8;
             bool ok = true;
+#pragma unroll 1
             for (int s = 0; s < ns; ++s, ++ks) {
                 const uint32_t st = ks % kQdRing;
                 if (!warp_wait(&full_k[st], (ks / kQdRing) & 1, abort_flag)) {
@@ -459,21 +468,22 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t kb = smem_u32(sm + kQsK + st * kSlabBytes);
-                    const uint32_t qb = q_base + s * 8192;
+                const uint64_t kd = smem_desc_sw128(smem_u32(sm + kQsK + st * kSlabBytes), 16, 1024);
+                const uint64_t qd = smem_desc_sw128(q_base + s * 8192, 16, 1024);
+                if (elect_one()) {
+                    // descriptors advance by 32 bytes (2 of their units) per step
+                    if (E8 && codes) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ad = smem_desc_sw128(kb + kk * 32, 16, 1024);
-                        const uint64_t bd = smem_desc_sw128(qb + kk * 32, 16, 1024);
-                        const uint32_t acc = (s | kk) ? 1u : 0u;
-                        if (comp) {
-                            mma_f8(dst, ad, bd, id_e, acc);
-                            mma_f8(dst, ad, smem_desc_sw128(qb + 32768 + kk * 32, 16, 1024), id_e, 1u);
-                            if (NORM) mma_f8(tmem + kTmKK, ad, ad, id_ekk, acc);
-                        } else {
-                            mma_ss(dst, ad, bd, id_w, acc);
-                            if (NORM) mma_ss(tmem + kTmKK, ad, ad, id_wkk, acc);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma_f8(dst, kd + 2 * kk, qd + 2 * kk, id_e, (s | kk) ? 1u : 0u);
+                            mma_f8(dst, kd + 2 * kk, qd + (32768 >> 4) + 2 * kk, id_e, 1u);
+                            if (NORM) mma_f8(tmem + kTmKK, kd + 2 * kk, kd + 2 * kk, id_ekk, (s | kk) ? 1u : 0u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma_ss(dst, kd + 2 * kk, qd + 2 * kk, id_w, (s | kk) ? 1u : 0u);
+                            if (NORM) mma_ss(tmem + kTmKK, kd + 2 * kk, kd + 2 * kk, id_wkk, (s | kk) ? 1u : 0u);
                         }
                     }
                     mma_commit(&empty_k[st]);
@@ -481,7 +491,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 mma_commit(&s_full[sb]);
                 if (it.qlast()) mma_commit(q_empty);
             }
@@ -490,62 +500,68 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         if (lane == 0 && nq) mbar_drain_wait(q_tma, (nq - 1) & 1);
         __syncwarp();
     } else if (warp == 2) {
-        // ===================================================== PV issuer (warp waits, lane 0 issues)
+        // ===================================================== PV issuer (warp waits, one lane issues)
         const uint32_t id_w = idesc_bf16(128, kDecHeads, 1, 1);
         const uint32_t id_hi = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE4M3, 1, 1);
         const uint32_t id_lo = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE5M2, 1, 1);
         uint32_t vs = 0;
         for (int n = 0; !it.done; it.next(), ++n) {
             const int b = n % kDecPBufs;
-            const bool first = it.first(), comp = it.comp();
+            const bool first = it.first(), codes = it.codes();
             if (!warp_wait(&p_full[b], (n / kDecPBufs) & 1, abort_flag)) break;
             if (first && !warp_wait(o_empty, (it.item & 1) ^ 1, abort_flag)) break;
             tc_fence_after();
             const int nvalid = it.nvalid();
             const uint32_t p_base = smem_u32(sm + kQsP + b * kDecPBytes);
-            const int per = comp ? 1 : 2;                  // slabs per 128-channel chunk
+            const int per = codes ? 1 : 2;                 // slabs per 128-channel chunk
+            const int step = codes ? 32 : 16;              // keys per MMA; steps without a key are left out
+            const int steps = (nvalid + step - 1) / step;
+            const int nz = (steps * step - nvalid) * 8;    // 16-byte chunks of rows in the last step without a key
             bool ok = true;
+#pragma unroll 1
             for (int c = 0; c < 4; ++c, vs += per) {
                 const uint32_t st = vs % kQdRing;          // per == 2: vs is even, the two slabs adjoin
                 for (int x = 0; ok && x < per; ++x)
                     ok = warp_wait(&full_v[st + x], (vs / kQdRing) & 1, abort_flag);
                 if (!ok) break;
                 uint8_t* slab = sm + kQsV + st * kSlabBytes;
-                if (nvalid < kDecTile) {
+                if (nz > 0) {
                     // rows >= nvalid may hold anything (memory past the visible entries, ring slots not
                     // yet written): zero them so 0-probability keys contribute exactly 0
-                    const int nz = (kDecTile - nvalid) * 8;
-                    for (int i = lane; i < per * nz; i += 32) {
-                        const int sl = i / nz, k = i - sl * nz;
-                        *reinterpret_cast<uint4*>(slab + sl * kSlabBytes + (nvalid + (k >> 3)) * 128 + (k & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
+#pragma unroll 1
+                    for (int sl = 0; sl < per; ++sl)
+#pragma unroll 1
+                        for (int i = lane; i < nz; i += 32)
+                            *reinterpret_cast<uint4*>(slab + sl * kSlabBytes + nvalid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t vb = smem_u32(slab);
-                    const uint32_t dst = tmem + kTmO + 64 * c;
-                    if (comp) {
+                const uint32_t dst = tmem + kTmO + 64 * c;
+                const uint64_t vd = smem_desc_sw128(smem_u32(slab), kSlabBytes, 1024);
+                const uint64_t p8 = smem_desc_sw64(p_base, 8192, 512), pw = smem_desc_sw128(p_base, 8192, 1024);
+                if (elect_one()) {
+                    if (E8 && codes) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {   // 32 keys each
-                            const uint64_t ad = smem_desc_sw128(vb + kk * 4096, kSlabBytes, 1024);
-                            mma_f8(dst, ad, smem_desc_sw64(p_base + kk * 2048, 8192, 512), id_hi, (first && kk == 0) ? 0u : 1u);
-                            mma_f8(dst, ad, smem_desc_sw64(p_base + 8192 + kk * 2048, 8192, 512), id_lo, 1u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk)     // 32 keys each
+                            if (kk < steps) {
+                                mma_f8(dst, vd + kk * (4096 >> 4), p8 + kk * (2048 >> 4), id_hi, (first && kk == 0) ? 0u : 1u);
+                                mma_f8(dst, vd + kk * (4096 >> 4), p8 + ((8192 + kk * 2048) >> 4), id_lo, 1u);
+                            }
+                        mma_commit(&empty_v[st]);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)     // 16 keys each
-                            mma_ss(dst, smem_desc_sw128(vb + kk * 2048, kSlabBytes, 1024),
-                                   smem_desc_sw128(p_base + kk * 2048, 8192, 1024), id_w, (first && kk == 0) ? 0u : 1u);
+                            if (kk < steps)
+                                mma_ss(dst, vd + kk * (2048 >> 4), pw + kk * (2048 >> 4), id_w, (first && kk == 0) ? 0u : 1u);
+                        mma_commit(&empty_v[st]);
+                        mma_commit(&empty_v[st + 1]);
                     }
-                    for (int x = 0; x < per; ++x) mma_commit(&empty_v[st + x]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) {
+            if (elect_one()) {
                 mma_commit(&p_empty[b]);
                 if (it.last()) mma_commit(o_full);
             }
@@ -559,9 +575,9 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         const int r = q4 * 32 + lane;                        // key row within the tile / channel within a chunk
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const int sidx = threadIdx.x - 32 * kQdSoftWarp0;    // 0..255
-        // the two scale bytes of this thread's key in the iterator's tile (1.0 for window tokens)
+        // the two scale bytes of this thread's key in the iterator's tile (1.0 for bf16 keys)
         auto scales = [&]() -> uint32_t {
-            if (it.done || !it.comp() || r >= it.nvalid()) return 0x7f7fu;
+            if (!E8 || it.done || !it.comp() || r >= it.nvalid()) return 0x7f7fu;
             const int j = it.tile * kDecTile + r;
             long long row;
             if (PAGED)
@@ -574,174 +590,140 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         float lsum[32];       // this thread's share of the row sums, per head
 #pragma unroll
         for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
-        bool ok = true;
-        for (int n = 0; ok && !it.done; ++n) {
-            const bool first = it.first(), last = it.last(), comp = it.comp();
+        // A wait of this warp ran out.  The warps leave together, at the barrier that every tile has; until then a
+        // warp that gave up goes on without waiting for long (the abort flag is set).
+        bool bad = false;
+        uint32_t nq = 0;
+        for (int n = 0; !it.done; ++n) {
+            const bool first = it.first(), last = it.last(), codes = it.codes();
             if (it.qfirst()) {
                 // ---- the query operand: q (with QK normalisation q / rms(q) * g_q * g_k, since q_hat . k_hat =
-                // (q' . k) / rms(k)), as two e4m3 terms for entries, in bf16 for the window.  Four threads per
-                // head, 128 channels each, held in registers between the read and the in-place write.
-                if (!group_wait(q_tma, it.qitem & 1, abort_flag)) { ok = false; break; }
-                const int h = sidx >> 2, part = sidx & 3;
-                float inv = 1.f;
-                auto chunk = [&](int i) {       // channels 128 part + 8 i .. + 7 of head h
-                    return reinterpret_cast<uint4*>(sm + kQsQ + (2 * part + (i >> 3)) * 8192 + sw128(h, i & 7));
-                };
-                if (NORM) {
-                    float ss = 0.f;
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 x = *chunk(i);
-                        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = bf16lo(w4[e]), b2 = bf16hi(w4[e]);
-                            ss = fmaf(a, a, fmaf(b2, b2, ss));
-                        }
-                    }
-                    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-                    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-                    inv = rsqrtf(ss * (1.f / kDecD) + p.eps);
-                }
-                // channels ch, ch + 1 of the query, from the bf16 pair w
-                auto value = [&](uint32_t w, int ch) {
-                    float2 a = make_float2(bf16lo(w), bf16hi(w));
+                // (q' . k) / rms(k)), as two e4m3 terms for codes, else in bf16.  A warp makes one head at a time, in
+                // place: the head's row of every slab is what its two 8-bit rows take.
+                if ((NORM || codes) && !bad) {
+                    bad = !warp_wait(q_tma, nq & 1, abort_flag);
+                    const int c0 = 16 * lane;                // this lane's channels
+                    float g[NORM ? 16 : 1];
                     if (NORM) {
-                        a.x *= inv * __ldg(p.gq + ch) * __ldg(p.gk + ch);
-                        a.y *= inv * __ldg(p.gq + ch + 1) * __ldg(p.gk + ch + 1);
-                    }
-                    return a;
-                };
-                if (comp) {
-                    float am = 0.f;
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 x = *chunk(i);
-                        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 a = value(w4[e], 128 * part + 8 * i + 2 * e);
-                            am = fmaxf(am, fmaxf(q_mag(a.x), q_mag(a.y)));
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 a = __ldg(reinterpret_cast<const float4*>(p.gq + c0 + e));
+                            const float4 b2 = __ldg(reinterpret_cast<const float4*>(p.gk + c0 + e));
+                            g[e] = a.x * b2.x;
+                            g[e + 1] = a.y * b2.y;
+                            g[e + 2] = a.z * b2.z;
+                            g[e + 3] = a.w * b2.w;
                         }
                     }
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                    const uint32_t byte = q_scale_byte(am);
-                    const float qi = q_inv_scale(byte);
-                    if (part == 0) qs_s[h] = q_scale(byte) * p.scale_log2;
-                    // the two terms take the rows' place: all of this thread's codes are made before any row
-                    // is overwritten
-                    uint32_t hi[32], lo[32];
+#pragma unroll 1
+                    for (int h = warp - kQdSoftWarp0; h < p.G && !bad; h += kDecSoftWarps) {
+                        uint4* src0 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3)));
+                        uint4* src1 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3) + 1));
+                        const uint4 xa = *src0, xb = *src1;
+                        const uint32_t w8[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                        float f[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 x = *chunk(i);
-                        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t hc[4], lc[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 a = value(w4[e], 128 * part + 8 * i + 2 * e);
-                            const float a0 = q_prep(a.x, qi), a1 = q_prep(a.y, qi);
-                            hc[e] = cvt_e4m3x2(a0, a1);
-                            const float2 f = e4m3x2_f32(hc[e]);
-                            lc[e] = cvt_e4m3x2(a0 - f.x, a1 - f.y);
+                        for (int e = 0; e < 8; ++e) {
+                            f[2 * e] = bf16lo(w8[e]);
+                            f[2 * e + 1] = bf16hi(w8[e]);
                         }
-                        hi[2 * i] = hc[0] | hc[1] << 16;
-                        hi[2 * i + 1] = hc[2] | hc[3] << 16;
-                        lo[2 * i] = lc[0] | lc[1] << 16;
-                        lo[2 * i + 1] = lc[2] | lc[3] << 16;
-                    }
-                    softmax_bar();           // every row has been read
+                        if (NORM) {
+                            float ss = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {        // 16 channels: one 16-byte chunk of hi and of lo
-                        uint8_t* dst = sm + kQsQ + part * 8192 + sw128(h, i);
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-                        *reinterpret_cast<uint4*>(dst + 32768) =
-                            make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+                            for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+                            ss = q_warp_sum(ss);
+                            const float inv = rsqrtf(ss * (1.f / kDecD) + p.eps);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) f[e] *= inv * g[e];
+                        }
+                        if (E8 && codes) {
+                            float am = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) am = fmaxf(am, q_mag(f[e]));
+                            // non-negative floats are ordered as their bits
+                            const uint32_t byte = q_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am))));
+                            const float qi = q_inv_scale(byte);
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t hp[2], lp[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const float a0 = q_prep(f[4 * e + 2 * x], qi), a1 = q_prep(f[4 * e + 2 * x + 1], qi);
+                                    hp[x] = cvt_e4m3x2(a0, a1);
+                                    const float2 b2 = e4m3x2_f32(hp[x]);
+                                    lp[x] = cvt_e4m3x2(a0 - b2.x, a1 - b2.y);
+                                }
+                                hi[e] = hp[0] | hp[1] << 16;
+                                lo[e] = lp[0] | lp[1] << 16;
+                            }
+                            __syncwarp();                    // every lane has read its part of the row
+                            uint8_t* dst = sm + kQsQ + (lane >> 3) * 8192 + sw128(h, lane & 7);
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(dst + 32768) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            if (lane == 0) qs_s[h] = q_scale(byte) * p.scale_log2;
+                        } else {
+                            *src0 = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                               pack_bf16x2(f[6], f[7]));
+                            *src1 = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]),
+                                               pack_bf16x2(f[14], f[15]));
+                        }
                     }
                     fence_proxy_async_smem();
-                    // a unit's entries come first in its piece: the sums start here
-#pragma unroll
-                    for (int hx = 0; hx < 32; ++hx) lsum[hx] = 0.f;
-                } else if (NORM) {
-                    if (part == 0) qs_s[h] = p.scale_log2;
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        uint4* ptr = chunk(i);
-                        const uint4 x = *ptr;
-                        uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 a = value(w4[e], 128 * part + 8 * i + 2 * e);
-                            w4[e] = pack_bf16x2(a.x, a.y);
-                        }
-                        *ptr = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                    }
-                    fence_proxy_async_smem();
-                } else if (sidx < 64) {
-                    qs_s[sidx] = p.scale_log2;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full);
                 }
+                ++nq;
+                if (!codes && sidx < 64) qs_s[sidx] = p.scale_log2;
                 softmax_bar();               // qs_s
-                if (lane == 0) mbar_arrive(q_full);
             }
 
             const int sb = n % look;
             const bool valid = r < it.nvalid();
-            if (!group_wait(&s_full[sb], (n / look) & 1, abort_flag)) { ok = false; break; }
+            if (!bad) bad = !warp_wait(&s_full[sb], (n / look) & 1, abort_flag);
             tc_fence_after();
             float z[32];
-            tmem_ld16(tmem + lane_off + dec_s_col(sb) + h0, z);
-            tmem_ld16(tmem + lane_off + dec_s_col(sb) + h0 + 16, z + 16);
+            tmem_ld32(tmem + lane_off + dec_s_col(sb) + h0, z);
             float kscale = q_scale(sc & 0xffu);
             if (NORM) {
                 float d[32];
-                tmem_ld16(tmem + lane_off + kTmKK + q4 * 32, d);
-                tmem_ld16(tmem + lane_off + kTmKK + q4 * 32 + 16, d + 16);
-                tmem_wait_ld();
+                tmem_ld32(tmem + lane_off + kTmKK + q4 * 32, d);
+                tmem_wait_ld32(d);
                 float diag = 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) diag = (j == lane) ? d[j] : diag;
                 kscale *= rsqrtf(diag * (1.f / kDecD) * kscale * kscale + p.eps);
-            } else {
-                tmem_wait_ld();
             }
+            tmem_wait_ld32(z);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[sb]);
             // y = logit + log2(vscale)
             const float lv = (float)((int)(sc >> 8) - 127);
             const float rv = q_inv_scale(sc >> 8);
+            bool need = first;
 #pragma unroll
             for (int h = 0; h < 32; h += 4) {
                 const float4 qs = *reinterpret_cast<const float4*>(qs_s + h0 + h);
+                const float4 mm = *reinterpret_cast<const float4*>(m_s + h0 + h);
                 z[h] = valid ? fmaf(z[h] * kscale, qs.x, lv) : -INFINITY;
                 z[h + 1] = valid ? fmaf(z[h + 1] * kscale, qs.y, lv) : -INFINITY;
                 z[h + 2] = valid ? fmaf(z[h + 2] * kscale, qs.z, lv) : -INFINITY;
                 z[h + 3] = valid ? fmaf(z[h + 3] * kscale, qs.w, lv) : -INFINITY;
+                need |= (z[h] > mm.x + thr) | (z[h + 1] > mm.y + thr) | (z[h + 2] > mm.z + thr) | (z[h + 3] > mm.w + thr);
             }
 
             // ---- reference m (shared m_s[64]): the first tile's maximum, then only when some y
-            // exceeds it by 2^8
-            bool need;
-            if (first) {
-                need = true;
-            } else {
-                bool mine = false;
-#pragma unroll
-                for (int h = 0; h < 32; h += 4) {
-                    const float4 mm = *reinterpret_cast<const float4*>(m_s + h0 + h);
-                    mine |= (z[h] > mm.x + kRescaleThreshold) | (z[h + 1] > mm.y + kRescaleThreshold) |
-                            (z[h + 2] > mm.z + kRescaleThreshold) | (z[h + 3] > mm.w + kRescaleThreshold);
-                }
-                need = softmax_any(mine);
-            }
-            if (need) {
+            // exceeds it by thr
+            if (softmax_any(need || bad)) {
+                if (softmax_any(bad)) break;
                 const float tmax = colreduce32<true>(z, lane);
                 red[q4 * 64 + h0 + lane] = tmax;
                 softmax_bar();
                 if (sidx < 64) {
                     const float mo = first ? -INFINITY : m_s[sidx];
                     const float mt = fmaxf(fmaxf(red[sidx], red[64 + sidx]), fmaxf(red[128 + sidx], red[192 + sidx]));
-                    const float mn = fmaxf(mo, mt - kQdShift);
+                    const float mn = fmaxf(mo, mt - shift);
                     al_s[sidx] = first ? 0.f : ex2(mo - mn);
                     m_s[sidx] = mn;
                 }
@@ -751,21 +733,19 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     for (int h = 0; h < 32; ++h) lsum[h] *= al_s[h0 + h];
                     // rescale O^T once the previous PV has landed
                     const int pb = (n - 1) % kDecPBufs;
-                    if (!group_wait(&p_empty[pb], ((n - 1) / kDecPBufs) & 1, abort_flag)) { ok = false; break; }
+                    bad = !warp_wait(&p_empty[pb], ((n - 1) / kDecPBufs) & 1, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-#pragma unroll 1
-                        for (int c16 = 0; c16 < 32; c16 += 16) {
-                            float o[16];
-                            const uint32_t ta = tmem + lane_off + kTmO + 64 * c + h0 + c16;
-                            tmem_ld16(ta, o);
-                            tmem_wait_ld();
-                            uint32_t w[16];
+                        float o[32];
+                        const uint32_t ta = tmem + lane_off + kTmO + 64 * c + h0;
+                        tmem_ld32(ta, o);
+                        tmem_wait_ld32(o);
+                        uint32_t w[32];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * al_s[h0 + c16 + j]);
-                            tmem_st16(ta, w);
-                        }
+                        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] * al_s[h0 + j]);
+                        tmem_st16(ta, w);
+                        tmem_st16(ta + 16, w + 16);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -783,33 +763,35 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 for (int e = 0; e < 4; ++e) lsum[h + e] = fmaf(z[h + e], rv, lsum[h + e]);
             }
             const int pbuf = n % kDecPBufs;
-            if (!group_wait(&p_empty[pbuf], ((n / kDecPBufs) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (!bad) bad = !warp_wait(&p_empty[pbuf], ((n / kDecPBufs) & 1) ^ 1, abort_flag);
             uint8_t* pt = sm + kQsP + pbuf * kDecPBytes;
-            if (comp) {
+            if (!bad) {
+                if (E8 && codes) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t hi[4], lo[4];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float* y = z + 16 * c + 4 * e;
-                        const uint32_t c0 = cvt_e4m3x2(y[0], y[1]), c1 = cvt_e4m3x2(y[2], y[3]);
-                        const float2 f0 = e4m3x2_f32(c0), f1 = e4m3x2_f32(c1);
-                        hi[e] = c0 | c1 << 16;
-                        lo[e] = cvt_e5m2x2(y[0] - f0.x, y[1] - f0.y) | cvt_e5m2x2(y[2] - f1.x, y[3] - f1.y) << 16;
+                        for (int e = 0; e < 4; ++e) {
+                            const float* y = z + 16 * c + 4 * e;
+                            const uint32_t c0 = cvt_e4m3x2(y[0], y[1]), c1 = cvt_e4m3x2(y[2], y[3]);
+                            const float2 f0 = e4m3x2_f32(c0), f1 = e4m3x2_f32(c1);
+                            hi[e] = c0 | c1 << 16;
+                            lo[e] = cvt_e5m2x2(y[0] - f0.x, y[1] - f0.y) | cvt_e5m2x2(y[2] - f1.x, y[3] - f1.y) << 16;
+                        }
+                        *reinterpret_cast<uint4*>(pt + sw64(r, 2 * hh + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(pt + 8192 + sw64(r, 2 * hh + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    *reinterpret_cast<uint4*>(pt + sw64(r, 2 * hh + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(pt + 8192 + sw64(r, 2 * hh + c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            } else {
+                } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(pt + sw128(r, 4 * hh + c)) =
-                        make_uint4(pack_bf16x2(z[8 * c], z[8 * c + 1]), pack_bf16x2(z[8 * c + 2], z[8 * c + 3]),
-                                   pack_bf16x2(z[8 * c + 4], z[8 * c + 5]), pack_bf16x2(z[8 * c + 6], z[8 * c + 7]));
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4*>(pt + sw128(r, 4 * hh + c)) =
+                            make_uint4(pack_bf16x2(z[8 * c], z[8 * c + 1]), pack_bf16x2(z[8 * c + 2], z[8 * c + 3]),
+                                       pack_bf16x2(z[8 * c + 4], z[8 * c + 5]), pack_bf16x2(z[8 * c + 6], z[8 * c + 7]));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[pbuf]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[pbuf]);
 
             if (last) {
                 // ---- end of this CTA's piece of unit u: the row sums over all key rows, then the
@@ -830,22 +812,18 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 softmax_bar();     // red[] is free again before the next piece's first reduction
 #pragma unroll
                 for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
-                if (!group_wait(o_full, it.item & 1, abort_flag)) { ok = false; break; }
+                if (!bad) bad = !warp_wait(o_full, it.item & 1, abort_flag);
                 tc_fence_after();
-                float* orec = p.rec_o + (size_t)rec * 64 * kDecD;
+                float* orec = p.rec_o + ((size_t)rec * 64 + h0) * kDecD + r;
+                const int hn = min(32, p.G - h0);        // heads of this half
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-#pragma unroll 1
-                    for (int c16 = 0; c16 < 32; c16 += 16) {
-                        float o[16];
-                        tmem_ld16(tmem + lane_off + kTmO + 64 * c + h0 + c16, o);
-                        tmem_wait_ld();
+                    float o[32];
+                    tmem_ld32(tmem + lane_off + kTmO + 64 * c + h0, o);
+                    tmem_wait_ld32(o);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int h = h0 + c16 + j;
-                            if (h < p.G) orec[(size_t)h * kDecD + 128 * c + r] = o[j];
-                        }
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (j < hn) orec[(size_t)j * kDecD + 128 * c] = o[j];
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -863,6 +841,8 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    // the merge follows this pass: its end is the prefix pass's end too
+    if (p.pfx_total > 0 && cta == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace hca

@@ -117,9 +117,9 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, uint64_t d0, uint64_t rows
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per (kernel slot, device).
 bool set_smem_attr_once(const void* fn, int bytes, int slot) {
     static std::mutex mu;
-    static bool done[24][64] = {};
+    static bool done[32][64] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || slot < 0 || slot >= 24) return false;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || slot < 0 || slot >= 32) return false;
     std::lock_guard<std::mutex> g(mu);
     if (done[slot][dev]) return true;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
@@ -370,58 +370,6 @@ size_t hca_decode_workspace_size(int B, int Hq, int Hkv, int dv) {
 
 namespace {
 
-// The split pass (decode.cuh) over a cache, window and workspace whose arguments have been checked; fills in the
-// launch's parameters (p.skip, p.pad and what only the second pass reads are the caller's).
-hca_status_t split_pass(hca::DecodeParams& p, const void* q, const void* kc, const void* vc, const int* page_table,
-                        int page_size, int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
-                        const float* gq, const float* gk, float eps, uint8_t* ws, const DecodeWs& lay, int nsplit, int B,
-                        int Hq, int Hkv, int blk, int W, int Nmax, float scale, unsigned flags, cudaStream_t s) {
-    using namespace hca;
-    const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM;
-    const uint64_t hd = (uint64_t)Hkv * kDecD;
-    CUtensorMap tq, tk, tv, tkw, tvw;
-    bool ok = true;
-    // queries [B, Hq, 512]: a box of 64 heads starting at the group's first head
-    ok &= make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
-    if (paged) {
-        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
-        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
-    } else {
-        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
-        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
-    }
-    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    if (!ok) return HCA_ERR_CUDA;
-
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.seqlens = seqlens;
-    p.page_table = paged ? page_table : nullptr;
-    p.gq = norm ? gq : nullptr;
-    p.gk = norm ? gk : nullptr;
-    p.total = reinterpret_cast<long long*>(ws);
-    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
-    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
-    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
-    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
-    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
-    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
-    p.flags = (int)flags; p.nsplit = nsplit;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.eps = eps;
-
-    // compile-time variants: QK normalisation x paged cache
-    using SplitFn = void (*)(const DecodeParams, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                             const CUtensorMap, const CUtensorMap);
-    const SplitFn split = norm ? (paged ? decode_split_kernel<true, true> : decode_split_kernel<true, false>)
-                               : (paged ? decode_split_kernel<false, true> : decode_split_kernel<false, false>);
-    if (!set_smem_attr_once(reinterpret_cast<const void*>(split), (int)kDecSmemBytes, 4 + 2 * norm + paged))
-        return HCA_ERR_CUDA;
-    split<<<nsplit, kDecThreads, kDecSmemBytes, s>>>(p, tq, tk, tv, tkw, tvw);
-    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
-    return HCA_OK;
-}
-
 // hca_decode and hca_decode_vha: the split kernel, then the combine kernel (merge, gate and,
 // with factors, Virtual Head Attention).
 hca_status_t decode_impl(const void* q, const void* kc, const void* vc, const int* page_table, int page_size,
@@ -468,16 +416,55 @@ hca_status_t decode_impl(const void* q, const void* kc, const void* vc, const in
     const DecodeWs lay = decode_ws_layout(U, nsplit);
     if (ws_bytes < lay.bytes) return HCA_ERR_INVALID_ARG;
 
-    DecodeParams p = {};
+    const uint64_t hd = (uint64_t)Hkv * kDecD;
+    CUtensorMap tq, tk, tv, tkw, tvw;
+    bool ok = true;
+    // queries [B, Hq, 512]: a box of 64 heads starting at the group's first head
+    ok &= make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
+    if (paged) {
+        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
+        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, page_size, num_pages, kDecD, hd, hd * page_size, 64, 1, 64, 1);
+    } else {
+        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
+        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, Nmax, B, kDecD, hd, hd * Nmax, 64, 1, 128, 1);
+    }
+    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    if (!ok) return HCA_ERR_CUDA;
+
+    DecodeParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.seqlens = seqlens;
+    p.page_table = paged ? page_table : nullptr;
+    p.gq = norm ? gq : nullptr;
+    p.gk = norm ? gk : nullptr;
     p.gate = gated ? static_cast<const __nv_bfloat16*>(gate) : nullptr;
     p.out = out;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.total = reinterpret_cast<long long*>(ws);
+    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
+    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
+    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
+    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
     p.vha_u = vha_u;
     p.vha_v = vha_v;
     p.vha_r = vha_u ? vha_r : 0;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    p.flags = (int)flags; p.nsplit = nsplit;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.eps = eps;
+
+    // compile-time variants: QK normalisation x paged cache
+    using SplitFn = void (*)(const DecodeParams, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                             const CUtensorMap, const CUtensorMap);
+    const SplitFn split = norm ? (paged ? decode_split_kernel<true, true> : decode_split_kernel<true, false>)
+                               : (paged ? decode_split_kernel<false, true> : decode_split_kernel<false, false>);
+    if (!set_smem_attr_once(reinterpret_cast<const void*>(split), (int)kDecSmemBytes, 4 + 2 * norm + paged))
+        return HCA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const hca_status_t st = split_pass(p, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps,
-                                       static_cast<uint8_t*>(workspace), lay, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
-    if (st != HCA_OK) return st;
+    split<<<nsplit, kDecThreads, kDecSmemBytes, s>>>(p, tq, tk, tv, tkw, tvw);
+    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)U, (unsigned)(kDecD / kMergeCh));
@@ -1045,7 +1032,6 @@ namespace {
 
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool pool_dim(int x) { return x == 64 || x == 128 || x == 256 || x == 512; }
 
 // Checks of a contiguous or paged cache's geometry, shared by the calls below.
@@ -1178,6 +1164,72 @@ extern "C" hca_status_t hca_read_quant(const void* kc, const void* vc, const voi
     return launch_status();
 }
 
+namespace {
+
+// The attention pass (decode_quant.cuh) over a cache of codes (E8) or of bf16 entries, a window and a workspace whose
+// arguments have been checked; fills in the launch's parameters (p.sc, p.skip and the plan's are the caller's).
+template <bool E8>
+hca_status_t attend_pass(hca::QuantParams& p, const void* q, const void* kc, const void* vc, const int* page_table,
+                         int page_size, int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
+                         const float* gq, const float* gk, float eps, uint8_t* ws, const DecodeWs& lay, int nsplit, int grid,
+                         int B, int Hq, int Hkv, int blk, int W, int Nmax, float scale, unsigned flags, cudaStream_t s) {
+    using namespace hca;
+    const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM;
+    const uint64_t hd = (uint64_t)Hkv * kDecD;
+    CUtensorMap tq, tk, tv, tkw, tvw;
+    bool ok = make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
+    const uint64_t rows = paged ? page_size : Nmax, outer = paged ? num_pages : B;
+    const uint32_t box = paged ? 64 : 128;
+    if (E8) {
+        ok &= make_tmap_4d_u8(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+        ok &= make_tmap_4d_u8(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+    } else {
+        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
+        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
+    }
+    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    if (!ok) return HCA_ERR_CUDA;
+
+    p.seqlens = seqlens;
+    p.page_table = paged ? page_table : nullptr;
+    p.gq = norm ? gq : nullptr;
+    p.gk = norm ? gk : nullptr;
+    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
+    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
+    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
+    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
+    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
+    p.cap = paged ? (int)((long long)max_pages * page_size) : Nmax;     // checked to fit
+    p.flags = (int)flags; p.nsplit = nsplit;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.eps = eps;
+    using Fn = void (*)(const QuantParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                        const CUtensorMap);
+    const Fn fn = norm ? (paged ? decode_quant_kernel<true, true, E8> : decode_quant_kernel<true, false, E8>)
+                       : (paged ? decode_quant_kernel<false, true, E8> : decode_quant_kernel<false, false, E8>);
+    if (!set_smem_attr_once(reinterpret_cast<const void*>(fn), (int)kQdSmem, (E8 ? 16 : 24) + 2 * norm + paged))
+        return HCA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kQdThreads);
+    cfg.dynamicSmemBytes = kQdSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.pfx_total > 0 ? 1 : 0;         // beside the prefix pass
+    if (cudaLaunchKernelEx(&cfg, fn, p, tq, tk, tv, tkw, tvw) != cudaSuccess) {
+        cudaGetLastError();
+        return HCA_ERR_CUDA;
+    }
+    return HCA_OK;
+}
+
+}  // namespace
+
 extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, const void* scales,
                                          const int* page_table, int page_size, int max_pages, int num_pages,
                                          const void* kw, const void* vw, const int* seqlens, const float* gq,
@@ -1198,7 +1250,7 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
         !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
         return HCA_ERR_INVALID_ARG;
     if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
-    if (norm && (!gq || !gk || !aligned4(gq) || !aligned4(gk))) return HCA_ERR_INVALID_ARG;
+    if (norm && (!gq || !gk || !aligned16(gq) || !aligned16(gk))) return HCA_ERR_INVALID_ARG;
     if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
     if (vha_u || vha_v) {
         if (!vha_u || !vha_v || vha_rank < 1 || !aligned4(vha_u) || !aligned4(vha_v)) return HCA_ERR_INVALID_ARG;
@@ -1211,41 +1263,13 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
     const DecodeWs lay = decode_ws_layout(U, nsplit);
     if (ws_bytes < lay.bytes) return HCA_ERR_INVALID_ARG;
 
-    const uint64_t hd = (uint64_t)Hkv * kDecD;
-    CUtensorMap tq, tk, tv, tkw, tvw;
-    bool ok = make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
-    const uint64_t rows = paged ? page_size : Nmax, outer = paged ? num_pages : B;
-    const uint32_t box = paged ? 64 : 128;
-    ok &= make_tmap_4d_u8(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
-    ok &= make_tmap_4d_u8(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
-    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    if (!ok) return HCA_ERR_CUDA;
-
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    QuantParams p;
-    p.seqlens = seqlens;
-    p.page_table = paged ? page_table : nullptr;
+    QuantParams p = {};
     p.sc = static_cast<const uint16_t*>(scales);
-    p.gq = norm ? gq : nullptr;
-    p.gk = norm ? gk : nullptr;
-    p.meta = reinterpret_cast<int*>(ws + lay.meta_off);
-    p.rec_m = reinterpret_cast<float*>(ws + lay.m_off);
-    p.rec_l = reinterpret_cast<float*>(ws + lay.l_off);
-    p.rec_o = reinterpret_cast<float*>(ws + lay.o_off);
-    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
-    p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
-    p.flags = (int)flags; p.nsplit = nsplit;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.eps = eps;
-    using Fn = void (*)(const QuantParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                        const CUtensorMap);
-    const Fn fn = norm ? (paged ? decode_quant_kernel<true, true> : decode_quant_kernel<true, false>)
-                       : (paged ? decode_quant_kernel<false, true> : decode_quant_kernel<false, false>);
-    if (!set_smem_attr_once(reinterpret_cast<const void*>(fn), (int)kQdSmem, 16 + 2 * norm + paged)) return HCA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    fn<<<nsplit, kQdThreads, kQdSmem, s>>>(p, tq, tk, tv, tkw, tvw);
-    if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
+    const hca_status_t st = attend_pass<true>(p, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk,
+                                              eps, static_cast<uint8_t*>(workspace), lay, nsplit, nsplit, B, Hq, Hkv, blk, W,
+                                              Nmax, scale, flags, s);
+    if (st != HCA_OK) return st;
 
     MergeParams mp = {};
     mp.seqlens = seqlens;
@@ -1381,7 +1405,7 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         !aligned16(vw) || !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
         return HCA_ERR_INVALID_ARG;
     if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
-    if (norm && (!gq || !gk || !aligned8(gq) || !aligned8(gk))) return HCA_ERR_INVALID_ARG;
+    if (norm && (!gq || !gk || !aligned16(gq) || !aligned16(gk))) return HCA_ERR_INVALID_ARG;
     if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
     if (vha_u || vha_v) {
         if (!vha_u || !vha_v || vha_rank < 1 || !aligned4(vha_u) || !aligned4(vha_v)) return HCA_ERR_INVALID_ARG;
@@ -1394,14 +1418,12 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
-    // the sequences' own entries and windows
-    DecodeParams dp = {};
+    QuantParams dp = {};
     dp.skip = Np;
-    dp.pad = 1;
-    hca_status_t st = split_pass(dp, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps, ws,
-                                 lay.own, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
-    if (st != HCA_OK) return st;
+    int grid = nsplit;
+    hca_status_t st;
 
+    int clusters = 0;
     MergeParams mp = {};
     if (Np > 0) {
         PrefixParams p = {};
@@ -1414,8 +1436,18 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         p.total = (long long)lay.row_tiles * lay.tiles;
         const int most = norm ? prefix_clusters<true>(s) : prefix_clusters<false>(s);
         if (most <= 0) return HCA_ERR_CUDA;
-        p.per = (p.total + most - 1) / most;
-        const int clusters = (int)((p.total + p.per - 1) / p.per);
+        // the plan goes by the lengths, which are on the device; the grids go by the fewest and the most own tiles
+        // that a batch of this shape can have
+        const long long cap = paged ? (long long)max_pages * page_size : (long long)Nmax;
+        const long long U = (long long)B * Hkv;
+        clusters = shared_plan(p.total, U, most, nsplit).clusters;
+        grid = shared_plan(p.total, U * ((cap + kDecTile - 1) / kDecTile + (W + kDecTile - 1) / kDecTile), most, nsplit).splits;
+        p.max_clusters = most;
+        p.sms = nsplit;
+        p.cap = (int)cap;
+        dp.pfx_total = p.total;
+        dp.pfx_max = most;
+        dp.plan = reinterpret_cast<SharedPlan*>(ws + 64);
         if (norm) {
             PrefixPrepParams pp = {};
             pp.q = static_cast<const __nv_bfloat16*>(q);
@@ -1451,8 +1483,14 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         mp.pfx_o = reinterpret_cast<const float*>(ws + lay.o_off);
         mp.tpt = p.tpt;
         mp.pfx_tiles = p.nct;
-        mp.pfx_per = p.per;
+        mp.pfx_total = p.total;
+        mp.pfx_clusters = clusters;
+        mp.plan = dp.plan;
     }
+    // the sequences' own entries and windows, beside the prefix pass where there is one
+    st = attend_pass<false>(dp, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps, ws, lay.own,
+                            nsplit, grid, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
+    if (st != HCA_OK) return st;
     mp.seqlens = seqlens;
     mp.meta = dp.meta;
     mp.rec_m = dp.rec_m;

@@ -15,6 +15,46 @@
 
 namespace hca {
 
+// hca_decode_shared's two passes share the GPU: how many clusters of four SMs attend the prefix, and how many CTAs
+// the sequences' own tiles.  Both passes, and the host for their grids, compute it from the same numbers.
+struct SharedPlan {
+    int clusters, splits;
+};
+
+// pfx: prefix tiles (256 rows x 256 keys); own: own tiles (128 keys of one sequence).  The plan with the shortest longer
+// pass, from measured times: a prefix tile takes a cluster about 2.8 us after 14 us of start and record, an own tile
+// takes one SM (its loads' latency) about 4 us after 18 us.
+__host__ __device__ inline long long shared_time(long long pfx, long long own, int c, int sms) {
+    const int ns = sms - 4 * c;
+    if (c > pfx || ns < 4) return 0x3fffffffffffffLL;
+    const long long tp = 140 + 28 * ((pfx + c - 1) / c), ts = 180 + 40 * ((own + ns - 1) / ns);
+    return tp > ts ? tp : ts;
+}
+inline SharedPlan shared_plan(long long pfx, long long own, int max_clusters, int sms) {
+    int best = 1;
+    for (int c = 2; c <= max_clusters; ++c)
+        if (shared_time(pfx, own, c, sms) < shared_time(pfx, own, best, sms)) best = c;
+    return SharedPlan{best, sms - 4 * best};
+}
+// The same by a whole warp (up to 255 clusters), on every lane.
+__device__ __forceinline__ SharedPlan shared_plan_warp(long long pfx, long long own, int max_clusters, int sms) {
+    long long key = 0x7fffffffffffffffLL;          // (time, clusters)
+    for (int c = (threadIdx.x & 31) + 1; c <= max_clusters; c += 32) {
+        const long long k = shared_time(pfx, own, c, sms) << 8 | c;
+        key = k < key ? k : key;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const long long k = __shfl_xor_sync(0xffffffffu, key, off);
+        key = k < key ? k : key;
+    }
+    const int c = (int)(key & 255);
+    return SharedPlan{c, sms - 4 * c};
+}
+
+// Prefix tiles in one cluster's range.
+__host__ __device__ inline long long pfx_per(long long total, int clusters) { return (total + clusters - 1) / clusters; }
+
 struct MergeParams {
     const int* seqlens;           // [B]
     const int* meta;              // [U][2]: first and last CTA holding a piece of unit u
@@ -30,9 +70,10 @@ struct MergeParams {
     void* out;                    // [B, Hq, 512]
     int vha_r, B, Hq, Hkv, G, nsplit, out_f32;
     // prefix records: a row tile holds 2 tpt sequences of one KV head, 128 rows for each tpt of them; its key tiles are
-    // numbers [rt * pfx_tiles, (rt + 1) * pfx_tiles) of the list that is cut into ranges of pfx_per tiles
-    int tpt, pfx_tiles;
-    long long pfx_per;
+    // numbers [rt * pfx_tiles, (rt + 1) * pfx_tiles) of the list that is cut into one range per cluster of the plan
+    int tpt, pfx_tiles, pfx_clusters;
+    long long pfx_total;
+    const SharedPlan* plan;
 };
 
 template <int kChunk, bool kVha, bool kPfx>
@@ -130,8 +171,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
         }
         if (kPfx && p.pfx_tiles > 0) {
             const int rt = (b / (2 * p.tpt)) * p.Hkv + g;
-            const int pf = (int)((long long)rt * p.pfx_tiles / p.pfx_per);
-            const int pl = (int)(((long long)(rt + 1) * p.pfx_tiles - 1) / p.pfx_per);
+            const long long per = pfx_per(p.pfx_total, min(__ldcg(&p.plan->clusters), p.pfx_clusters));
+            const int pf = (int)((long long)rt * p.pfx_tiles / per);
+            const int pl = (int)(((long long)(rt + 1) * p.pfx_tiles - 1) / per);
             fold(1, pf, pl, (size_t)rt, (b / p.tpt & 1) * 128 + (b % p.tpt) * p.G + hh, 256);
         }
         const float inv = 1.f / L;

@@ -21,6 +21,7 @@
 
 #include <cuda_fp16.h>
 
+#include "merge.cuh"
 #include "prefill_pair.cuh"
 
 namespace hca {
@@ -31,7 +32,8 @@ struct PrefixParams {
     float* pfx_m;                 // [clusters + row tiles][256] references
     float* pfx_l;                 // sums of 2^(z - m)
     int B, Hq, Hkv, G, tpt, blk, W, Np, nct;
-    long long total, per;         // pairs of the list, and of a cluster's range
+    long long total;              // pairs of the list
+    int max_clusters, sms, cap;   // for shared_plan; own entries that a sequence's cache can hold
     float scale_log2;
 };
 
@@ -54,6 +56,13 @@ __device__ __forceinline__ PfxPiece pfx_piece(const PrefixParams& p, long long x
 }
 __device__ __forceinline__ int pfx_keys(const PrefixParams& p, const PfxPiece& it, int j) {
     return min(kPpKeys, p.Np - kPpKeys * (it.j0 + j));
+}
+// Tiles of 128 keys of a sequence's own entries and window (as q_unit of decode_quant.cuh counts them).
+__device__ __forceinline__ long long own_tiles(int L, int W, int blk, int Np, long long cap) {
+    L = max(L, 1);
+    const long long a = (long long)L - W, n0 = a > 0 ? a / blk : 0;
+    const long long n = min(n0 > Np ? n0 - Np : 0, cap);
+    return (n + kDecTile - 1) / kDecTile + (min(L, W) + kDecTile - 1) / kDecTile;
 }
 // Prefix entries visible to row r of an SM's half of the tile (= sequence * G + head); rows without a sequence see none.
 __device__ __forceinline__ int pfx_visible(const PrefixParams& p, const PfxPiece& it, int half, int r) {
@@ -270,6 +279,16 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
         }
     }
     if (warp == 1) px_tmem_alloc(tmem_slot);
+    // the own pass may start beside this one
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 2) {
+        long long own = 0;
+        for (int b = lane; b < p.B; b += 32) own += own_tiles(__ldg(p.seqlens + b), p.W, p.blk, p.Np, p.cap);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) own += __shfl_xor_sync(0xffffffffu, own, off);
+        const SharedPlan plan = shared_plan_warp(p.total, own * p.Hkv, p.max_clusters, p.sms);
+        if (lane == 0) misc[3] = min((int)(gridDim.x >> 2), plan.clusters);
+    }
     tc_fence_before();
     __syncthreads();
     pp_cluster_sync();      // every CTA's barriers are initialised before any remote arrive
@@ -282,7 +301,8 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
     for (uint32_t c = 0; c < 4; ++c) go &= pp_ld_cluster_u32(pp_mapa(smem_u32(misc + 2), c)) != 0;
     if (!go && threadIdx.x == 0) record_error(HCA_ERR_INTERNAL);
     const int cl = blockIdx.x >> 2;               // this cluster's range of the list of (row tile, key tile)
-    const long long x_beg = cl * p.per, x_end = min(p.total, x_beg + p.per);
+    const long long per = pfx_per(p.total, misc[3]);
+    const long long x_beg = min(p.total, cl * per), x_end = min(p.total, x_beg + per);
 
     if (s_cta && warp == 0) {
         // ===================================================== S pair: TMA of Q and K

@@ -409,7 +409,7 @@ hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales,
  * hca_decode_quant -- hca_decode over an 8-bit compressed cache and a raw bf16 window: the attention of
  * the entries' values code * 2^e.  kc, vc, scales contiguous [B,Nmax,Hkv,..] or page pools with HCA_PAGED;
  * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v [Hq, vha_rank] fp32 for the mixing of
- * hca_decode_vha (Hkv == 1), else NULL; every other argument, the workspace (hca_decode_workspace_size)
+ * hca_decode_vha (Hkv == 1), else NULL; gq, gk 16-byte aligned; every other argument, the workspace (hca_decode_workspace_size)
  * and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row: its output is zero.
  * Arithmetic: codes go to the tensor cores as they are; the query and the probabilities are split into
  * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.
@@ -429,7 +429,7 @@ hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, con
  * j < Np and row j - Np of the sequence's own cache (kc, vc: contiguous [B,Nmax,Hkv,512] or pages) from there on;
  * visibility goes by seqlens (which count the prefix's tokens) as in hca_decode, so a sequence that is still
  * inside the prefix sees only the part before its window.  Np == 0 is a batch without a prefix (kp, vp NULL).
- * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v as for hca_decode_quant; gq, gk 8-byte aligned;
+ * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v, gq, gk as for hca_decode_quant;
  * every other argument and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row:
  * its output is zero.  The workspace: hca_decode_shared_workspace_size bytes.
  */
