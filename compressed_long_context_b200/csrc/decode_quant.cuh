@@ -47,6 +47,8 @@ constexpr int kQdSoftWarp0 = 4;
 constexpr int kQdRing = 4;                 // slabs per ring (K, V)
 constexpr int kQdLook = 4;                 // S buffers (2 with QK normalisation)
 constexpr int kQdLookNorm = 2;
+constexpr int kQdKept = 2048;              // units whose tile counts fit the P buffers while these are not in use
+constexpr int kQdAhead = 3;                // tiles whose slabs are requested into L2 ahead of the rings
 constexpr float kQdShift = 6.0f;           // the reference m lies this far (log2) below the maximum
 
 constexpr uint32_t kQsQ = 0;
@@ -61,6 +63,7 @@ constexpr uint32_t kQsAlpha = kQsMax + 64 * 4;                      // float[64]
 constexpr uint32_t kQsQscale = kQsAlpha + 64 * 4;                   // float[64] query scale * logit scale (log2)
 constexpr uint32_t kQsMisc = kQsQscale + 64 * 4;
 constexpr uint32_t kQdSmem = kQsMisc + 128;
+static_assert(kQdKept * 8 <= kDecPBufs * kDecPBytes, "kept tile counts fit the P buffers");
 static_assert(kQdSmem <= 232448, "decode_quant shared memory exceeds the 227 KB per-block limit");
 static_assert(kQsRed % 16 == 0 && kQsK % 1024 == 0 && kQsV % 1024 == 0, "alignment");
 
@@ -84,51 +87,66 @@ struct QuantParams {
     float scale_log2, eps;
 };
 
+// Keys of a sequence of length L: nc own entries visible (clamped into the cache), nw window tokens.
+struct QKeys {
+    int nc, nw;
+};
+
+// Not inlined: a dozen callers share its code, which the first of them fetches.
+__device__ __noinline__ QKeys q_keys_of(int L, int W, int blk, int skip, int cap, bool report) {
+    if (L < 1) {                                     // 0: a padding row (its merge writes zeros)
+        if (report && L < 0) record_error(HCA_ERR_DEVICE_INPUT);
+        L = 1;
+    }
+    const int a = L - W;                           // (t - W + 1) with t = L - 1
+    int nc = (a > 0 ? (int)((unsigned)a / (unsigned)blk) : 0) - skip;
+    nc = nc > 0 ? nc : 0;
+    if (nc > cap) {
+        if (report) record_error(HCA_ERR_DEVICE_INPUT);
+        nc = cap;
+    }
+    return QKeys{nc, L < W ? L : W};
+}
+__device__ __forceinline__ QKeys q_keys(const QuantParams& p, int L, bool report) {
+    return q_keys_of(L, p.W, p.blk, p.skip, p.cap, report);
+}
+
+__device__ __forceinline__ float q_warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 // A unit's tiles: nct tiles of 128 entries (cost 1 each), then nwt tiles of 128 raw window tokens (cost
-// wc: 2 beside codes, which have half the bytes, else 1).
-struct QUnit {
-    int b, g, nc, nw, nct, nwt, s0;
+// WC: 2 beside codes, which have half the bytes, else 1).  All counts of a batch fit 31 bits (checked on the host).
+struct QTiles {
+    int nct, nwt;
     __device__ __forceinline__ int tiles() const { return nct + nwt; }
     template <int WC> __device__ __forceinline__ int cost() const { return nct + WC * nwt; }
     // first tile that starts at or after cost position x
     template <int WC> __device__ __forceinline__ int tile_at(int x) const { return x <= nct ? x : nct + (x - nct + WC - 1) / WC; }
 };
-
-__device__ __forceinline__ QUnit q_unit(const QuantParams& p, int u, bool report) {
-    QUnit t;
-    t.b = u / p.Hkv;
-    t.g = u - t.b * p.Hkv;
-    int L = __ldg(p.seqlens + t.b);
-    if (L < 1) {                                     // 0: a padding row (its merge writes zeros)
-        if (report && L < 0) record_error(HCA_ERR_DEVICE_INPUT);
-        L = 1;
-    }
-    const int a = L - p.W;                           // (t - W + 1) with t = L - 1
-    int nc = (a > 0 ? (int)((unsigned)a / (unsigned)p.blk) : 0) - p.skip;
-    nc = nc > 0 ? nc : 0;
-    if (nc > p.cap) {
-        if (report) record_error(HCA_ERR_DEVICE_INPUT);
-        nc = p.cap;
-    }
-    t.nc = nc;
-    t.nw = L < p.W ? L : p.W;
-    t.nct = (t.nc + kDecTile - 1) / kDecTile;
-    t.nwt = (t.nw + kDecTile - 1) / kDecTile;
-    t.s0 = (p.flags & HCA_WINDOW_RING) ? 0 : p.W - t.nw;
-    return t;
+__device__ __forceinline__ QTiles q_tiles(const QKeys& k) {
+    return QTiles{(k.nc + kDecTile - 1) / kDecTile, (k.nw + kDecTile - 1) / kDecTile};
 }
+__device__ __forceinline__ int q_seq(const QuantParams& p, int u) { return p.Hkv == 1 ? u : u / p.Hkv; }
 
 // A CTA's range: either tiles [beg, end) of unit u (`aligned`), or the tiles that start in the cost range [beg, end) of
 // the batch's list, in which unit u starts at pu.
 struct QRange {
-    long long beg, end, pu;
-    int u, aligned;
+    int beg, end, pu, u, aligned;
 };
 
-template <typename T>
-__device__ __forceinline__ T q_warp_sum(T v) {
+// x * i / k without leaving 32 bits (i <= k < 2^15)
+__device__ __forceinline__ int q_part(int x, int i, int k) { return x / k * i + x % k * i / k; }
+
+__device__ __forceinline__ int q_scan(int v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int off = 1; off < 32; off <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += n;
+    }
     return v;
 }
 
@@ -139,104 +157,97 @@ __device__ __forceinline__ T q_warp_sum(T v) {
 //  - otherwise equal cost ranges of at least the cost of a window tile, so that every CTA between a unit's first
 //    and last holds one of its tiles and leaves a record.
 template <int WC>
-__device__ __noinline__ void q_range(const QuantParams& p, int cta, int grid, QRange* out) {
+__device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid, QRange* out, uint2* kept) {
     const int lane = threadIdx.x & 31;
     const int U = p.B * p.Hkv;
-    long long total = 0;
+    // the first kQdKept units' tile counts are kept in shared memory for the passes below
+    int total = 0;
 #pragma unroll 1
-    for (int u = lane; u < U; u += 32) total += q_unit(p, u, true).cost<WC>();
-    total = q_warp_sum(total);
+    for (int u0 = lane; u0 < U; u0 += 128) {
+        int L[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) L[i] = u0 + 32 * i < U ? __ldg(p.seqlens + q_seq(p, u0 + 32 * i)) : 1;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const int u = u0 + 32 * i;
+            if (u >= U) break;
+            const QTiles t = q_tiles(q_keys(p, i == 0 ? L[0] : i == 1 ? L[1] : i == 2 ? L[2] : L[3], true));
+            total += t.cost<WC>();
+            if (u < kQdKept) kept[u] = make_uint2(t.nct, t.nwt);
+        }
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    __syncwarp();
+    auto tiles_of = [&](int u) {
+        if (u < kQdKept) {
+            const uint2 t = kept[u];
+            return QTiles{(int)t.x, (int)t.y};
+        }
+        return q_tiles(q_keys(p, __ldg(p.seqlens + q_seq(p, u)), false));
+    };
     int nsplit = p.nsplit;
     if (p.pfx_total > 0) {
         const SharedPlan plan = shared_plan_warp(p.pfx_total, total, p.pfx_max, p.nsplit);
         nsplit = min(plan.splits, grid);
         if (lane == 0 && cta == 0) *p.plan = plan;
     }
-    const long long tpc = max((long long)WC, (total + nsplit - 1) / nsplit);
-    QRange r = {min(total, tpc * cta), min(total, tpc * (cta + 1)), 0, -1, 0};
-    int T = 0;
-    if (U <= nsplit && nsplit < 0x4000 && total <= 0x3fffffffll) {
-        // the four candidate counts are summed in one reduction, as 16-bit fields: k_u <= nsplit * cost_u / total + 2
-        // (fl rounds in fp32: one more), so each sum is at most nsplit + 3 U < 2^16
-        const float share = (float)nsplit / (float)total;
-        auto count = [&](const QUnit& t, int w) {
-            const unsigned c = t.cost<WC>(), Tw = (unsigned)tpc + w;
-            return max(1, min(t.tiles(), max((int)((float)c * share), (int)((c + Tw - 1u) / Tw))));
-        };
-        unsigned long long sum = 0;
+    const int tpc = max(WC, (int)(((unsigned)total + nsplit - 1u) / (unsigned)nsplit));
+    QRange r = {(int)min((long long)total, (long long)tpc * cta), (int)min((long long)total, (long long)tpc * (cta + 1)), 0, -1, 0};
+    int w = 4;
+    const float share = (float)nsplit / (float)total;
+    auto count = [&](const QTiles& t, int x) {
+        const int c = t.cost<WC>();
+        return max(1, min(t.tiles(), max((int)((float)c * share), (int)(((unsigned)c + (unsigned)(tpc + x) - 1u) / (unsigned)(tpc + x)))));
+    };
+    if (U <= nsplit && nsplit < 0x2000) {
+        // two candidate counts to a word: k_u <= nsplit * cost_u / total + 2 (one more for the rounding of `share`), so
+        // each sum is at most nsplit + 3 U < 2^15
 #pragma unroll 1
-        for (int u = lane; u < U; u += 32) {
-            const QUnit t = q_unit(p, u, false);
+        for (int x = 0; x < 4 && w == 4; x += 2) {
+            unsigned sum = 0;
 #pragma unroll 1
-            for (int w = 0; w < 4; ++w) sum += (unsigned long long)count(t, w) << (16 * w);
-        }
-        sum = q_warp_sum(sum);
-        int w = 0;
-        while (w < 4 && (int)((sum >> (16 * w)) & 0xffffu) > nsplit) ++w;
-        if (w < 4) {
-            T = 1;
-            int base = 0;
-            r.beg = r.end = 0;
-#pragma unroll 1
-            for (int u0 = 0; u0 < U && base <= cta; u0 += 32) {
-                const int u = u0 + lane;
-                QUnit t = {};
-                int k = 0;
-                if (u < U) {
-                    t = q_unit(p, u, false);
-                    k = count(t, w);
-                }
-                int incl = k;
-#pragma unroll 1
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int n = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += n;
-                }
-                const int i = cta - (base + incl - k);
-                const bool mine = i >= 0 && i < k;
-                if (mine) {
-                    const int c = t.cost<WC>(), n = t.tiles();
-                    r.u = u;
-                    if (WC * k <= c) {                  // every cost range holds a tile's start
-                        r.beg = t.tile_at<WC>((int)((long long)c * i / k));
-                        r.end = t.tile_at<WC>((int)((long long)c * (i + 1) / k));
-                    } else {                            // near one tile per CTA: even tile counts
-                        r.beg = n * i / k;
-                        r.end = n * (i + 1) / k;
-                    }
-                    r.aligned = 1;
-                    *out = r;
-                }
-                if (__any_sync(0xffffffffu, mine)) return;
-                base += __shfl_sync(0xffffffffu, incl, 31);
+            for (int u = lane; u < U; u += 32) {
+                const QTiles t = tiles_of(u);
+                sum += (unsigned)count(t, x) | (unsigned)count(t, x + 1) << 16;
             }
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            w = (int)(sum & 0xffffu) <= nsplit ? x : (int)(sum >> 16) <= nsplit ? x + 1 : 4;
         }
     }
-    if (!T && r.beg < r.end) {
-        // the unit holding cost position beg
-        long long base = 0;
+    // the unit that holds this CTA (aligned: in the list of counts) or cost position beg
+    const int at = w < 4 ? cta : r.beg;
+    int base = 0;
+    bool found = w == 4 && r.beg >= r.end;
+    if (w < 4) r.beg = r.end = 0;
 #pragma unroll 1
-        for (int u0 = 0; u0 < U; u0 += 32) {
-            const int u = u0 + lane;
-            const int c = u < U ? q_unit(p, u, false).cost<WC>() : 0;
-            int incl = c;
-#pragma unroll 1
-            for (int off = 1; off < 32; off <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += n;
-            }
-            const long long pu = base + incl - c;
-            const bool mine = pu <= r.beg && r.beg < pu + c;
-            if (mine) {
-                r.u = u;
-                r.pu = pu;
-                *out = r;
-            }
-            if (__any_sync(0xffffffffu, mine)) return;
-            base += __shfl_sync(0xffffffffu, incl, 31);
+    for (int u0 = 0; u0 < U && !found; u0 += 32) {
+        const int u = u0 + lane;
+        QTiles t = {};
+        int n = 0;
+        if (u < U) {
+            t = tiles_of(u);
+            n = w < 4 ? count(t, w) : t.cost<WC>();
         }
+        const int incl = q_scan(n);
+        const int i = at - (base + incl - n);
+        const bool mine = i >= 0 && i < n;
+        if (mine) {
+            r.u = u;
+            r.pu = base + incl - n;
+            if (w < 4) {
+                const int c = t.cost<WC>(), m = t.tiles();
+                const bool even = WC * n > c;           // near one tile per CTA: even tile counts, else every cost
+                r.beg = even ? q_part(m, i, n) : t.tile_at<WC>(q_part(c, i, n));           // range holds a tile's start
+                r.end = even ? q_part(m, i + 1, n) : t.tile_at<WC>(q_part(c, i + 1, n));
+                r.aligned = 1;
+            }
+            *out = r;
+        }
+        found = __any_sync(0xffffffffu, mine);
+        if (found) return;
+        base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) *out = r;                            // nothing to do
+    if (lane == 0) *out = r;                            // nothing to do (u = -1)
 }
 
 // This CTA's tiles in order.
@@ -244,18 +255,35 @@ template <bool E8>
 struct QIter {
     static constexpr int WC = E8 ? 2 : 1;
     const QuantParams* p;
-    long long ce, pu;              // end of the range; cost position where unit u starts
-    QUnit t;
-    int u, tb, tend, tile, item;
+    int ce, pu;                    // end of the range; cost position where unit u starts
+    struct {
+        int b, g, nc, nw, nct, s0;
+    } t;
+    int u, tb, tend, ntiles, tile, item;
     bool fixed, done;
 
-    __device__ void load(long long from) {
-        t = q_unit(*p, u, false);
-        tb = t.template tile_at<WC>((int)((from > pu ? from : pu) - pu));
-        const long long end = pu + t.template cost<WC>();
-        tend = t.template tile_at<WC>((int)((ce < end ? ce : end) - pu));
+    __device__ __forceinline__ void load(int from, const QRange* r) {
+        t.b = q_seq(*p, u);
+        t.g = u - t.b * p->Hkv;
+        const QKeys k = q_keys(*p, __ldg(p->seqlens + t.b), false);
+        const QTiles n = q_tiles(k);
+        t.nc = k.nc;
+        t.nw = k.nw;
+        t.nct = n.nct;
+        t.s0 = (p->flags & HCA_WINDOW_RING) ? 0 : p->W - k.nw;
+        ntiles = n.tiles();
+        const int cost = n.template cost<WC>();
+        if (fixed && r) {
+            tb = r->beg;
+            tend = r->end;
+        } else {
+            tb = n.template tile_at<WC>(max(from - pu, 0));
+            tend = n.template tile_at<WC>(min(ce - pu, cost));
+        }
         tile = tb;
+        next_pu = pu + cost;
     }
+    int next_pu;
     __device__ __forceinline__ void init(const QuantParams* pp, const QRange& r) {
         p = pp;
         u = r.u;
@@ -265,24 +293,18 @@ struct QIter {
         item = 0;
         done = r.u < 0 || r.beg >= r.end;
         if (done) return;
-        if (fixed) {
-            t = q_unit(*p, u, false);
-            tb = tile = (int)r.beg;
-            tend = (int)r.end;
-        } else {
-            load(r.beg);
-            if (tb >= tend) advance();
-        }
+        load(r.beg, &r);
+        if (tb >= tend) advance();
     }
-    __device__ __forceinline__ void advance() {            // to the next unit with a tile in the range
+    __device__ __forceinline__ void advance() {         // to the next unit with a tile in the range
         do {
-            pu += t.template cost<WC>();
+            pu = next_pu;
             ++u;
             if (fixed || pu >= ce) {
                 done = true;
                 return;
             }
-            load(pu);
+            load(pu, nullptr);
         } while (tb >= tend);
     }
     __device__ bool first() const { return tile == tb; }
@@ -352,14 +374,13 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
     constexpr float shift = E8 ? kQdShift : 0.f, thr = E8 ? kRescaleThreshold : 32.f;
 
     if (warp == 2) {
-        q_range<E8 ? 2 : 1>(p, cta, gridDim.x, range);
+        q_range<E8 ? 2 : 1>(p, cta, gridDim.x, range, reinterpret_cast<uint2*>(sm + kQsP));
     } else if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
-    } else if (threadIdx.x == 0) {
-        *abort_flag = 0;
+    } else if (warp == 0) {
+        if (lane == 0) *abort_flag = 0;
         // barriers in order: full / empty of K, of V; q_tma, q_full, q_empty; s_full; s_empty; p_full; p_empty; o_full, o_empty
-#pragma unroll 1
-        for (int i = 0; i < kQdBars; ++i) {
+        for (int i = lane; i < kQdBars; i += 32) {
             const int j = i - 4 * kQdRing;
             const bool many = j == 1 || (j >= 3 + kQdLook && j < 3 + 2 * kQdLook + kDecPBufs) || i == kQdBars - 1;
             mbar_init(&full_k[i], many ? kDecSoftWarps : 1);
@@ -391,19 +412,45 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             const CUtensorMap* mw = is_v ? &tm_vw : &tm_kw;
             // test switch (hca_debug_set_drop_slab): the first K slab is never requested
             const bool drop = !is_v && *reinterpret_cast<volatile int*>(&g_debug_drop_slab) != 0;
+            // one slab of the iterator's tile: into L2 (dst null) or into a ring slot
+            int pg[2] = {0, 0};
+            auto pages = [&](const QIter<E8>& i, bool report) {
+                if (!PAGED || !i.comp()) return;
+                const int j0 = i.tile * kDecTile;
+                pg[0] = q_page(p, i.t.b, j0, report);
+                pg[1] = j0 + 64 < i.t.nc ? q_page(p, i.t.b, j0 + 64, report) : pg[0];
+            };
+            auto slab = [&](const QIter<E8>& i, int s, uint8_t* dst, uint64_t* bar) {
+                const bool comp = i.comp();
+                const CUtensorMap* m = comp ? mc : mw;
+                const int x = (i.codes() ? 128 : 64) * s, j0 = i.tile * kDecTile;
+                if (PAGED && comp) {
+                    const bool h1 = j0 + 64 < i.t.nc;
+                    if (dst) mbar_arrive_expect_tx(bar, h1 ? kSlabBytes : kSlabBytes / 2);
+#pragma unroll 1
+                    for (int h = 0; h < 1 + h1; ++h) {
+                        const int row = (j0 + 64 * h) % p.page_size, page = h ? pg[1] : pg[0];
+                        if (dst) tma_load_4d(dst + h * 8192, m, bar, x, i.t.g, row, page);
+                        else tma_prefetch_4d(m, x, i.t.g, row, page);
+                    }
+                } else {
+                    const int row = comp ? j0 : i.t.s0 + (i.tile - i.t.nct) * kDecTile;
+                    if (dst) {
+                        mbar_arrive_expect_tx(bar, kSlabBytes);
+                        tma_load_4d(dst, m, bar, x, i.t.g, row, i.t.b);
+                    } else {
+                        tma_prefetch_4d(m, x, i.t.g, row, i.t.b);
+                    }
+                }
+            };
             uint32_t n = 0;
+            int ahead = 0;
+            QIter<E8> pf = it;
+            if (!pf.done) pf.next();
             bool ok = true;
             for (; ok && !it.done; it.next()) {
-                const bool comp = it.comp(), halves = PAGED && comp;
-                int pg[2] = {0, 0};
-                const int j0 = it.tile * kDecTile;
-                const bool h1 = j0 + 64 < it.t.nc;
-                if (halves) {
-                    pg[0] = q_page(p, it.t.b, j0, true);
-                    pg[1] = h1 ? q_page(p, it.t.b, j0 + 64, true) : pg[0];
-                }
-                const int ns = it.codes() ? 4 : 8, wide = it.codes() ? 128 : 64;
-                const int row = comp ? j0 : it.t.s0 + (it.tile - it.t.nct) * kDecTile;
+                pages(it, true);
+                const int ns = it.codes() ? 4 : 8;
 #pragma unroll 1
                 for (int s = 0; s < ns; ++s, ++n) {
                     const uint32_t st = n % kQdRing;
@@ -411,15 +458,16 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                         ok = false;                                                  // consumer's wait runs out
                         break;
                     }
-                    uint8_t* dst = ring + st * kSlabBytes;
-                    mbar_arrive_expect_tx(&full[st], halves && !h1 ? kSlabBytes / 2 : kSlabBytes);
-                    if (halves) {
-                        tma_load_4d(dst, mc, &full[st], wide * s, it.t.g, j0 % p.page_size, pg[0]);
-                        if (h1) tma_load_4d(dst + 8192, mc, &full[st], wide * s, it.t.g, (j0 + 64) % p.page_size, pg[1]);
-                    } else {
-                        tma_load_4d(dst, comp ? mc : mw, &full[st], wide * s, it.t.g, row, it.t.b);
-                    }
+                    slab(it, s, ring + st * kSlabBytes, &full[st]);
                 }
+                // while the first tiles are waited for and worked on, memory streams the next ones into L2
+                for (; ok && ahead < kQdAhead && !pf.done; pf.next(), ++ahead) {
+                    pages(pf, false);
+                    const int np = pf.codes() ? 4 : 8;
+#pragma unroll 1
+                    for (int s = 0; s < np; ++s) slab(pf, s, nullptr, nullptr);
+                }
+                --ahead;
             }
             mbar_drain_ring(full, n, kQdRing);
         }
@@ -525,11 +573,14 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     ok = warp_wait(&full_v[st + x], (vs / kQdRing) & 1, abort_flag);
                 if (!ok) break;
                 uint8_t* slab = sm + kQsV + st * kSlabBytes;
-                if (nz > 0) {
+                if (nz > 0 && st == 0) {
                     // rows >= nvalid may hold anything (memory past the visible entries, ring slots not
-                    // yet written): zero them so 0-probability keys contribute exactly 0
+                    // yet written): zero them in all four slabs so 0-probability keys contribute exactly 0
 #pragma unroll 1
-                    for (int sl = 0; sl < per; ++sl)
+                    for (int x = per; ok && x < kQdRing; ++x) ok = warp_wait(&full_v[x], (vs / kQdRing) & 1, abort_flag);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int sl = 0; sl < kQdRing; ++sl)
 #pragma unroll 1
                         for (int i = lane; i < nz; i += 32)
                             *reinterpret_cast<uint4*>(slab + sl * kSlabBytes + nvalid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
@@ -575,10 +626,10 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         const int r = q4 * 32 + lane;                        // key row within the tile / channel within a chunk
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const int sidx = threadIdx.x - 32 * kQdSoftWarp0;    // 0..255
-        // the two scale bytes of this thread's key in the iterator's tile (1.0 for bf16 keys)
-        auto scales = [&]() -> uint32_t {
-            if (!E8 || it.done || !it.comp() || r >= it.nvalid()) return 0x7f7fu;
-            const int j = it.tile * kDecTile + r;
+        // the two scale bytes of this thread's key in tile `tile` of the iterator's unit (1.0 for bf16 keys)
+        auto scales = [&](int tile) -> uint32_t {
+            const int j = tile * kDecTile + r;
+            if (!E8 || it.done || j >= it.t.nc) return 0x7f7fu;
             long long row;
             if (PAGED)
                 row = (long long)q_page(p, it.t.b, j, false) * p.page_size + j % p.page_size;
@@ -586,7 +637,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 row = (long long)it.t.b * p.Nmax + j;
             return __ldg(p.sc + row * p.Hkv + it.t.g);
         };
-        uint32_t sc = scales();
+        uint32_t sc = scales(it.tile);
         float lsum[32];       // this thread's share of the row sums, per head
 #pragma unroll
         for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
@@ -601,7 +652,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 // (q' . k) / rms(k)), as two e4m3 terms for codes, else in bf16.  A warp makes one head at a time, in
                 // place: the head's row of every slab is what its two 8-bit rows take.
                 if ((NORM || codes) && !bad) {
-                    bad = !warp_wait(q_tma, nq & 1, abort_flag);
+                    bad = !warp_wait(q_tma, nq & 1, abort_flag);        // (an operand of garbage is never used then)
                     const int c0 = 16 * lane;                // this lane's channels
                     float g[NORM ? 16 : 1];
                     if (NORM) {
@@ -615,8 +666,9 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                             g[e + 3] = a.w * b2.w;
                         }
                     }
-#pragma unroll 1
-                    for (int h = warp - kQdSoftWarp0; h < p.G && !bad; h += kDecSoftWarps) {
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const int h = warp - kQdSoftWarp0 + kDecSoftWarps * i;
                         uint4* src0 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3)));
                         uint4* src1 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3) + 1));
                         const uint4 xa = *src0, xb = *src1;
@@ -637,25 +689,30 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                             for (int e = 0; e < 16; ++e) f[e] *= inv * g[e];
                         }
                         if (E8 && codes) {
-                            float am = 0.f;
+                            float am = 0.f;                  // (fmaxf leaves NaN out)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) am = fmaxf(am, q_mag(f[e]));
+                            for (int e = 0; e < 16; ++e) am = fmaxf(am, fabsf(f[e]));
                             // non-negative floats are ordered as their bits
-                            const uint32_t byte = q_scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am))));
+                            uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+                            if (top == 0x7f800000u) {        // an infinity: it becomes NaN, and the rest sets the scale
+                                am = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    am = fmaxf(am, q_mag(f[e]));
+                                    f[e] = q_prep(f[e], 1.f);
+                                }
+                                top = __reduce_max_sync(0xffffffffu, __float_as_uint(am));
+                            }
+                            const uint32_t byte = q_scale_byte(__uint_as_float(top));
                             const float qi = q_inv_scale(byte);
                             uint32_t hi[4], lo[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                uint32_t hp[2], lp[2];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    const float a0 = q_prep(f[4 * e + 2 * x], qi), a1 = q_prep(f[4 * e + 2 * x + 1], qi);
-                                    hp[x] = cvt_e4m3x2(a0, a1);
-                                    const float2 b2 = e4m3x2_f32(hp[x]);
-                                    lp[x] = cvt_e4m3x2(a0 - b2.x, a1 - b2.y);
-                                }
-                                hi[e] = hp[0] | hp[1] << 16;
-                                lo[e] = lp[0] | lp[1] << 16;
+                                uint32_t l0, l1;
+                                const uint32_t h0c = q_split(f[4 * e] * qi, f[4 * e + 1] * qi, l0);
+                                const uint32_t h1c = q_split(f[4 * e + 2] * qi, f[4 * e + 3] * qi, l1);
+                                hi[e] = h0c | h1c << 16;
+                                lo[e] = l0 | l1 << 16;
                             }
                             __syncwarp();                    // every lane has read its part of the row
                             uint8_t* dst = sm + kQsQ + (lane >> 3) * 8192 + sw128(h, lane & 7);
@@ -680,6 +737,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 
             const int sb = n % look;
             const bool valid = r < it.nvalid();
+            const uint32_t sc_next = last ? 0u : scales(it.tile + 1);      // loaded while this tile is worked on
             if (!bad) bad = !warp_wait(&s_full[sb], (n / look) & 1, abort_flag);
             tc_fence_after();
             float z[32];
@@ -803,7 +861,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 softmax_bar();
                 if (sidx == 0) {
                     if (it.tb == 0) p.meta[2 * u] = cta;
-                    if (it.tend == it.t.tiles()) p.meta[2 * u + 1] = cta;
+                    if (it.tend == it.ntiles) p.meta[2 * u + 1] = cta;
                 }
                 if (sidx < 64) {
                     p.rec_m[(size_t)rec * 64 + sidx] = m_s[sidx];
@@ -830,7 +888,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 if (lane == 0) mbar_arrive(o_empty);
             }
             it.next();
-            sc = scales();
+            sc = last ? scales(it.tile) : sc_next;
         }
     }
 

@@ -59,6 +59,22 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t c) {
     return f;
 }
 
+// Two values (at most 448 in magnitude, or NaN) as two e4m3 terms each: returns the codes of the values, sets those of what
+// is left.  The difference is taken in fp16, which holds 11 bits of the value and the code exactly.
+__device__ __forceinline__ uint32_t q_split(float a, float b, uint32_t& rest) {
+    uint32_t out, r;
+    asm("{\n\t.reg .b32 v, c, n;\n\t.reg .b16 h, l;\n\t"
+        "cvt.rn.f16x2.f32 v, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, v;\n\t"
+        "cvt.rn.f16x2.e4m3x2 c, h;\n\t"
+        "sub.f16x2 n, v, c;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, n;\n\t"
+        "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+        : "=r"(out), "=r"(r) : "f"(a), "f"(b));
+    rest = r;
+    return out;
+}
+
 // A code for x * inv: NaN for a value that is not finite.  (x * inv is at most 448 in magnitude for
 // every finite x that took part in the maximum.)
 __device__ __forceinline__ float q_prep(float x, float inv) { return fabsf(x) < INFINITY ? x * inv : NAN; }

@@ -6,9 +6,10 @@
 // 2^(z - m) and the 512 sums of 2^(z - m) v.  hca_decode_shared adds a second kind: the shared prefix
 // of 2 * (128 / G) sequences at once.
 //
-// Grid (units, 512 / 32), 128 threads: a CTA owns all G heads of one unit for 32 channels, thread =
-// (head, 16 channels), so the mixing across heads stays on chip.  The records of a chunk are all
-// loaded before any is used (one memory round trip for up to kChunk of them).
+// Grid (units, 512 / 32), 128 threads: a CTA owns all G heads of one unit for 32 channels, so the mixing across
+// heads stays on chip.  Thread = (4 channels, heads hb, hb + 16, hb + 32, hb + 48): a warp reads whole 128-byte
+// lines of four heads.  The records of a chunk are all loaded before any is used (one memory round trip for up to
+// kChunk of them).
 #pragma once
 
 #include "decode.cuh"
@@ -76,26 +77,28 @@ struct MergeParams {
     const SharedPlan* plan;
 };
 
+constexpr int kMergeHeads = 4;            // heads per thread
+
 template <int kChunk, bool kVha, bool kPfx>
 __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
     extern __shared__ float cs[];
     const int u = blockIdx.x;
-    const int h = threadIdx.x >> 1;
-    const int c16 = 16 * (threadIdx.x & 1);
-    const int c = blockIdx.y * kMergeCh + c16;                      // channels c .. c+15
-    const int b = u / p.Hkv, g = u - (u / p.Hkv) * p.Hkv;
-    const bool live = h < p.G;
-    const size_t orow = ((size_t)b * p.Hq + (size_t)g * p.G + (live ? h : 0)) * kDecD + c;
+    const int hb = threadIdx.x >> 3;
+    const int c4 = 4 * (threadIdx.x & 7);
+    const int c = blockIdx.y * kMergeCh + c4;                       // channels c .. c+3
+    const int b = p.Hkv == 1 ? u : u / p.Hkv, g = u - b * p.Hkv;
+    const size_t orow = ((size_t)b * p.Hq + (size_t)g * p.G + hb) * kDecD + c;
     const int R = p.vha_r;
     float* os = cs;                                   // [64][32] merged, gated outputs (16-byte rows)
     float* ts = os + kDecHeads * kMergeCh;            // [R][32]  V^T o
     float* vs = ts + R * kMergeCh;                    // [G][R]
     float* us = vs + kDecHeads * R;                   // [G][R]
     // the inputs are not products of the passes before: read while those still run
-    uint4 graw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (p.gate && live) {
-        graw[0] = __ldg(reinterpret_cast<const uint4*>(p.gate + orow));
-        graw[1] = __ldg(reinterpret_cast<const uint4*>(p.gate + orow) + 1);
+    uint2 graw[kMergeHeads];
+#pragma unroll
+    for (int x = 0; x < kMergeHeads; ++x) {
+        graw[x] = make_uint2(0, 0);
+        if (p.gate && hb + 16 * x < p.G) graw[x] = __ldg(reinterpret_cast<const uint2*>(p.gate + orow + (size_t)16 * x * kDecD));
     }
     const int len = __ldg(p.seqlens + b);
     if (kVha) {
@@ -105,141 +108,132 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float r[16];
+    float4 r[kMergeHeads];
     if (*reinterpret_cast<volatile unsigned int*>(&g_error) == HCA_ERR_TIMEOUT) {
         // a CTA gave up: its records may be stale, so the outputs are marked invalid
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = NAN;
+        for (int x = 0; x < kMergeHeads; ++x) r[x] = make_float4(NAN, NAN, NAN, NAN);
     } else if (len <= 0) {
         // a padding row (length 0; negative lengths are reported by the first pass)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = 0.f;
+        for (int x = 0; x < kMergeHeads; ++x) r[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     } else {
-        float M = -INFINITY, L = 0.f;
-        float acc[16];
+        float M[kMergeHeads], L[kMergeHeads];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-        // `kind` 0: the unit's own records; 1: the prefix records of its row tile
-        auto fold = [&](int kind, int first, int last, size_t rec0, int row, int stride) {
-            const float* pm = kind ? p.pfx_m : p.rec_m;
-            const float* pl = kind ? p.pfx_l : p.rec_l;
-            const float* po = kind ? p.pfx_o : p.rec_o;
+        for (int x = 0; x < kMergeHeads; ++x) {
+            M[x] = -INFINITY;
+            L[x] = 0.f;
+            r[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        // records rec0 + first .. rec0 + last of `stride` rows, of which this unit's heads start at `row`
+        auto fold = [&](const float* pm, const float* pl, const float* po, int first, int last, size_t rec0, int row, int stride) {
+#pragma unroll 1
             for (int i0 = first; i0 <= last; i0 += kChunk) {
-                float m[kChunk], l[kChunk];
-                float4 o[kChunk][4];
+                float m[kChunk][kMergeHeads], l[kChunk][kMergeHeads];
+                float4 o[kChunk][kMergeHeads];
 #pragma unroll
-                for (int k = 0; k < kChunk; ++k) {
-                    const bool ok = live && i0 + k <= last;   // ranges are contiguous: every one has a record
-                    const size_t rec = (rec0 + (size_t)(i0 + k)) * stride + row;
-                    m[k] = ok ? __ldcg(pm + rec) : -INFINITY;
-                    l[k] = ok ? __ldcg(pl + rec) : 0.f;
-                    const float4* op = reinterpret_cast<const float4*>(po + rec * kDecD + c);
+                for (int k = 0; k < kChunk; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[k][j] = ok ? __ldcg(op + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-                float Mn = M;
-#pragma unroll
-                for (int k = 0; k < kChunk; ++k) Mn = fmaxf(Mn, m[k]);
-                if (Mn == -INFINITY) continue;
-                const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn);
-                L *= sc;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) acc[j] *= sc;
-#pragma unroll
-                for (int k = 0; k < kChunk; ++k) {
-                    // a record without a visible key (m = -inf) holds nothing: its sums are not used
-                    if (m[k] == -INFINITY) continue;
-                    const float w = exp2f(m[k] - Mn);
-                    L = fmaf(w, l[k], L);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[4 * j] = fmaf(w, o[k][j].x, acc[4 * j]);
-                        acc[4 * j + 1] = fmaf(w, o[k][j].y, acc[4 * j + 1]);
-                        acc[4 * j + 2] = fmaf(w, o[k][j].z, acc[4 * j + 2]);
-                        acc[4 * j + 3] = fmaf(w, o[k][j].w, acc[4 * j + 3]);
+                    for (int x = 0; x < kMergeHeads; ++x) {
+                        // ranges are contiguous: every record is there
+                        const bool ok = hb + 16 * x < p.G && i0 + k <= last;
+                        const size_t rec = (rec0 + (size_t)(i0 + k)) * stride + row + hb + 16 * x;
+                        m[k][x] = ok ? __ldcg(pm + rec) : -INFINITY;
+                        l[k][x] = ok ? __ldcg(pl + rec) : 0.f;
+                        o[k][x] = ok ? __ldcg(reinterpret_cast<const float4*>(po + rec * kDecD + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+#pragma unroll
+                for (int x = 0; x < kMergeHeads; ++x) {
+                    float Mn = M[x];
+#pragma unroll
+                    for (int k = 0; k < kChunk; ++k) Mn = fmaxf(Mn, m[k][x]);
+                    if (Mn == -INFINITY) continue;
+                    const float sc = M[x] == -INFINITY ? 0.f : exp2f(M[x] - Mn);
+                    L[x] *= sc;
+                    r[x] = make_float4(r[x].x * sc, r[x].y * sc, r[x].z * sc, r[x].w * sc);
+#pragma unroll
+                    for (int k = 0; k < kChunk; ++k) {
+                        // a record without a visible key (m = -inf) holds nothing: its sums are not used
+                        if (m[k][x] == -INFINITY) continue;
+                        const float w = exp2f(m[k][x] - Mn);
+                        L[x] = fmaf(w, l[k][x], L[x]);
+                        r[x].x = fmaf(w, o[k][x].x, r[x].x);
+                        r[x].y = fmaf(w, o[k][x].y, r[x].y);
+                        r[x].z = fmaf(w, o[k][x].z, r[x].z);
+                        r[x].w = fmaf(w, o[k][x].w, r[x].w);
+                    }
+                    M[x] = Mn;
                 }
-                M = Mn;
             }
         };
-        const int hh = live ? h : 0;
         const int first = __ldcg(p.meta + 2 * u), last = __ldcg(p.meta + 2 * u + 1);
         if (first < 0 || last < first || last >= p.nsplit) {
             if (threadIdx.x == 0 && blockIdx.y == 0) record_error(HCA_ERR_DEVICE_INPUT);
         } else {
-            fold(0, first, last, (size_t)u, hh, kDecHeads);
+            fold(p.rec_m, p.rec_l, p.rec_o, first, last, (size_t)u, 0, kDecHeads);
         }
         if (kPfx && p.pfx_tiles > 0) {
             const int rt = (b / (2 * p.tpt)) * p.Hkv + g;
             const long long per = pfx_per(p.pfx_total, min(__ldcg(&p.plan->clusters), p.pfx_clusters));
             const int pf = (int)((long long)rt * p.pfx_tiles / per);
             const int pl = (int)(((long long)(rt + 1) * p.pfx_tiles - 1) / per);
-            fold(1, pf, pl, (size_t)rt, (b / p.tpt & 1) * 128 + (b % p.tpt) * p.G + hh, 256);
+            fold(p.pfx_m, p.pfx_l, p.pfx_o, pf, pl, (size_t)rt, (b / p.tpt & 1) * 128 + (b % p.tpt) * p.G, 256);
         }
-        const float inv = 1.f / L;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = acc[j] * inv;
-        if (p.gate) {
-            const uint32_t gw[8] = {graw[0].x, graw[0].y, graw[0].z, graw[0].w,
-                                    graw[1].x, graw[1].y, graw[1].z, graw[1].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                r[2 * j] *= __frcp_rn(1.f + __expf(-bf16lo(gw[j])));
-                r[2 * j + 1] *= __frcp_rn(1.f + __expf(-bf16hi(gw[j])));
+        for (int x = 0; x < kMergeHeads; ++x) {
+            const float inv = 1.f / L[x];
+            r[x] = make_float4(r[x].x * inv, r[x].y * inv, r[x].z * inv, r[x].w * inv);
+            if (p.gate) {
+                r[x].x *= __frcp_rn(1.f + __expf(-bf16lo(graw[x].x)));
+                r[x].y *= __frcp_rn(1.f + __expf(-bf16hi(graw[x].x)));
+                r[x].z *= __frcp_rn(1.f + __expf(-bf16lo(graw[x].y)));
+                r[x].w *= __frcp_rn(1.f + __expf(-bf16hi(graw[x].y)));
             }
         }
     }
     if (kVha) {
         // o'[:, ch] = o[:, ch] + U (V^T o[:, ch]) over the G heads of this token (see decode.cuh)
-        if (h < kDecHeads) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4*>(os + h * kMergeCh + c16 + 4 * j) =
-                    live ? make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3])
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int x = 0; x < kMergeHeads; ++x)
+            if (hb + 16 * x < p.G) *reinterpret_cast<float4*>(os + (hb + 16 * x) * kMergeCh + c4) = r[x];
         __syncthreads();
         for (int i = threadIdx.x; i < R * (kMergeCh / 4); i += 128) {
-            const int k = i >> 3, c4 = (i & 7) * 4;
+            const int k = i >> 3, cc = (i & 7) * 4;
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int hd = 0; hd < p.G; ++hd) {
                 const float vk = vs[hd * R + k];
-                const float4 o4 = *reinterpret_cast<const float4*>(os + hd * kMergeCh + c4);
+                const float4 o4 = *reinterpret_cast<const float4*>(os + hd * kMergeCh + cc);
                 t.x = fmaf(vk, o4.x, t.x);
                 t.y = fmaf(vk, o4.y, t.y);
                 t.z = fmaf(vk, o4.z, t.z);
                 t.w = fmaf(vk, o4.w, t.w);
             }
-            *reinterpret_cast<float4*>(ts + k * kMergeCh + c4) = t;
+            *reinterpret_cast<float4*>(ts + k * kMergeCh + cc) = t;
         }
         __syncthreads();
-        if (live) {
-            for (int k = 0; k < R; ++k) {
-                const float uk = us[h * R + k];
+        for (int k = 0; k < R; ++k) {
+            const float4 t4 = *reinterpret_cast<const float4*>(ts + k * kMergeCh + c4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 t4 = *reinterpret_cast<const float4*>(ts + k * kMergeCh + c16 + 4 * j);
-                    r[4 * j] = fmaf(uk, t4.x, r[4 * j]);
-                    r[4 * j + 1] = fmaf(uk, t4.y, r[4 * j + 1]);
-                    r[4 * j + 2] = fmaf(uk, t4.z, r[4 * j + 2]);
-                    r[4 * j + 3] = fmaf(uk, t4.w, r[4 * j + 3]);
-                }
+            for (int x = 0; x < kMergeHeads; ++x) {
+                if (hb + 16 * x >= p.G) continue;
+                const float uk = us[(hb + 16 * x) * R + k];
+                r[x].x = fmaf(uk, t4.x, r[x].x);
+                r[x].y = fmaf(uk, t4.y, r[x].y);
+                r[x].z = fmaf(uk, t4.z, r[x].z);
+                r[x].w = fmaf(uk, t4.w, r[x].w);
             }
         }
     }
-    if (!live) return;
-    if (p.out_f32) {
-        float* o = static_cast<float*>(p.out) + orow;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4*>(o + 4 * j) = make_float4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-    } else {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            o[j] = make_uint4(pack_bf16x2(r[8 * j], r[8 * j + 1]), pack_bf16x2(r[8 * j + 2], r[8 * j + 3]),
-                              pack_bf16x2(r[8 * j + 4], r[8 * j + 5]), pack_bf16x2(r[8 * j + 6], r[8 * j + 7]));
+    for (int x = 0; x < kMergeHeads; ++x) {
+        if (hb + 16 * x >= p.G) continue;
+        const size_t at = orow + (size_t)16 * x * kDecD;
+        if (p.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = r[x];
+        else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                make_uint2(pack_bf16x2(r[x].x, r[x].y), pack_bf16x2(r[x].z, r[x].w));
     }
 }
 
