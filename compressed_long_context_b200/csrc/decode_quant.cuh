@@ -48,7 +48,9 @@ constexpr int kQdRing = 4;                 // slabs per ring (K, V)
 constexpr int kQdLook = 4;                 // S buffers (2 with QK normalisation)
 constexpr int kQdLookNorm = 2;
 constexpr int kQdKept = 2048;              // units whose tile counts fit the P buffers while these are not in use
-constexpr int kQdAhead = 3;                // tiles whose slabs are requested into L2 ahead of the rings
+// Cost of starting a unit, in tiles: query operand, refilled pipeline and record take about 8 us, a tile 4 us where all
+// SMs stream.  It lies before the unit's first tile, so a range that starts units holds fewer tiles.
+constexpr int kQdStart = 2;
 constexpr float kQdShift = 6.0f;           // the reference m lies this far (log2) below the maximum
 
 constexpr uint32_t kQsQ = 0;
@@ -123,8 +125,10 @@ struct QTiles {
     int nct, nwt;
     __device__ __forceinline__ int tiles() const { return nct + nwt; }
     template <int WC> __device__ __forceinline__ int cost() const { return nct + WC * nwt; }
-    // first tile that starts at or after cost position x
-    template <int WC> __device__ __forceinline__ int tile_at(int x) const { return x <= nct ? x : nct + (x - nct + WC - 1) / WC; }
+    // first tile that starts at or after cost position x (from the first tile on)
+    template <int WC> __device__ __forceinline__ int tile_at(int x) const {
+        return x <= nct ? max(x, 0) : nct + (x - nct + WC - 1) / WC;
+    }
 };
 __device__ __forceinline__ QTiles q_tiles(const QKeys& k) {
     return QTiles{(k.nc + kDecTile - 1) / kDecTile, (k.nw + kDecTile - 1) / kDecTile};
@@ -155,7 +159,7 @@ __device__ __forceinline__ int q_scan(int v) {
 //    for the smallest cost per CTA T in tpc .. tpc + 3 whose counts fit the grid; every CTA then holds one piece
 //    (one query load, one record);
 //  - otherwise equal cost ranges of at least the cost of a window tile, so that every CTA between a unit's first
-//    and last holds one of its tiles and leaves a record.
+//    tile and its last holds one of its tiles and leaves a record.
 template <int WC>
 __device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid, QRange* out, uint2* kept) {
     const int lane = threadIdx.x & 31;
@@ -191,8 +195,7 @@ __device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid,
         nsplit = min(plan.splits, grid);
         if (lane == 0 && cta == 0) *p.plan = plan;
     }
-    const int tpc = max(WC, (int)(((unsigned)total + nsplit - 1u) / (unsigned)nsplit));
-    QRange r = {(int)min((long long)total, (long long)tpc * cta), (int)min((long long)total, (long long)tpc * (cta + 1)), 0, -1, 0};
+    int tpc = (int)(((unsigned)total + nsplit - 1u) / (unsigned)nsplit);
     int w = 4;
     const float share = (float)nsplit / (float)total;
     auto count = [&](const QTiles& t, int x) {
@@ -215,10 +218,16 @@ __device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid,
         }
     }
     // the unit that holds this CTA (aligned: in the list of counts) or cost position beg
+    QRange r = {0, 0, 0, -1, 0};
+    if (w == 4) {
+        total += kQdStart * U;
+        tpc = max(WC, (int)(((unsigned)total + nsplit - 1u) / (unsigned)nsplit));
+        r.beg = (int)min((long long)total, (long long)tpc * cta);
+        r.end = (int)min((long long)total, (long long)tpc * (cta + 1));
+    }
     const int at = w < 4 ? cta : r.beg;
     int base = 0;
     bool found = w == 4 && r.beg >= r.end;
-    if (w < 4) r.beg = r.end = 0;
 #pragma unroll 1
     for (int u0 = 0; u0 < U && !found; u0 += 32) {
         const int u = u0 + lane;
@@ -226,7 +235,7 @@ __device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid,
         int n = 0;
         if (u < U) {
             t = tiles_of(u);
-            n = w < 4 ? count(t, w) : t.cost<WC>();
+            n = w < 4 ? count(t, w) : kQdStart + t.cost<WC>();
         }
         const int incl = q_scan(n);
         const int i = at - (base + incl - n);
@@ -272,13 +281,13 @@ struct QIter {
         t.nct = n.nct;
         t.s0 = (p->flags & HCA_WINDOW_RING) ? 0 : p->W - k.nw;
         ntiles = n.tiles();
-        const int cost = n.template cost<WC>();
+        const int cost = kQdStart + n.template cost<WC>();
         if (fixed && r) {
             tb = r->beg;
             tend = r->end;
         } else {
-            tb = n.template tile_at<WC>(max(from - pu, 0));
-            tend = n.template tile_at<WC>(min(ce - pu, cost));
+            tb = n.template tile_at<WC>(from - pu - kQdStart);
+            tend = n.template tile_at<WC>(min(ce - pu, cost) - kQdStart);
         }
         tile = tb;
         next_pu = pu + cost;
@@ -412,45 +421,19 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             const CUtensorMap* mw = is_v ? &tm_vw : &tm_kw;
             // test switch (hca_debug_set_drop_slab): the first K slab is never requested
             const bool drop = !is_v && *reinterpret_cast<volatile int*>(&g_debug_drop_slab) != 0;
-            // one slab of the iterator's tile: into L2 (dst null) or into a ring slot
-            int pg[2] = {0, 0};
-            auto pages = [&](const QIter<E8>& i, bool report) {
-                if (!PAGED || !i.comp()) return;
-                const int j0 = i.tile * kDecTile;
-                pg[0] = q_page(p, i.t.b, j0, report);
-                pg[1] = j0 + 64 < i.t.nc ? q_page(p, i.t.b, j0 + 64, report) : pg[0];
-            };
-            auto slab = [&](const QIter<E8>& i, int s, uint8_t* dst, uint64_t* bar) {
-                const bool comp = i.comp();
-                const CUtensorMap* m = comp ? mc : mw;
-                const int x = (i.codes() ? 128 : 64) * s, j0 = i.tile * kDecTile;
-                if (PAGED && comp) {
-                    const bool h1 = j0 + 64 < i.t.nc;
-                    if (dst) mbar_arrive_expect_tx(bar, h1 ? kSlabBytes : kSlabBytes / 2);
-#pragma unroll 1
-                    for (int h = 0; h < 1 + h1; ++h) {
-                        const int row = (j0 + 64 * h) % p.page_size, page = h ? pg[1] : pg[0];
-                        if (dst) tma_load_4d(dst + h * 8192, m, bar, x, i.t.g, row, page);
-                        else tma_prefetch_4d(m, x, i.t.g, row, page);
-                    }
-                } else {
-                    const int row = comp ? j0 : i.t.s0 + (i.tile - i.t.nct) * kDecTile;
-                    if (dst) {
-                        mbar_arrive_expect_tx(bar, kSlabBytes);
-                        tma_load_4d(dst, m, bar, x, i.t.g, row, i.t.b);
-                    } else {
-                        tma_prefetch_4d(m, x, i.t.g, row, i.t.b);
-                    }
-                }
-            };
             uint32_t n = 0;
-            int ahead = 0;
-            QIter<E8> pf = it;
-            if (!pf.done) pf.next();
             bool ok = true;
             for (; ok && !it.done; it.next()) {
-                pages(it, true);
-                const int ns = it.codes() ? 4 : 8;
+                const bool comp = it.comp(), halves = PAGED && comp;
+                int pg[2] = {0, 0};
+                const int j0 = it.tile * kDecTile;
+                const bool h1 = j0 + 64 < it.t.nc;
+                if (halves) {
+                    pg[0] = q_page(p, it.t.b, j0, true);
+                    pg[1] = h1 ? q_page(p, it.t.b, j0 + 64, true) : pg[0];
+                }
+                const int ns = it.codes() ? 4 : 8, wide = it.codes() ? 128 : 64;
+                const int row = comp ? j0 : it.t.s0 + (it.tile - it.t.nct) * kDecTile;
 #pragma unroll 1
                 for (int s = 0; s < ns; ++s, ++n) {
                     const uint32_t st = n % kQdRing;
@@ -458,16 +441,15 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                         ok = false;                                                  // consumer's wait runs out
                         break;
                     }
-                    slab(it, s, ring + st * kSlabBytes, &full[st]);
+                    uint8_t* dst = ring + st * kSlabBytes;
+                    mbar_arrive_expect_tx(&full[st], halves && !h1 ? kSlabBytes / 2 : kSlabBytes);
+                    if (halves) {
+                        tma_load_4d(dst, mc, &full[st], wide * s, it.t.g, j0 % p.page_size, pg[0]);
+                        if (h1) tma_load_4d(dst + 8192, mc, &full[st], wide * s, it.t.g, (j0 + 64) % p.page_size, pg[1]);
+                    } else {
+                        tma_load_4d(dst, comp ? mc : mw, &full[st], wide * s, it.t.g, row, it.t.b);
+                    }
                 }
-                // while the first tiles are waited for and worked on, memory streams the next ones into L2
-                for (; ok && ahead < kQdAhead && !pf.done; pf.next(), ++ahead) {
-                    pages(pf, false);
-                    const int np = pf.codes() ? 4 : 8;
-#pragma unroll 1
-                    for (int s = 0; s < np; ++s) slab(pf, s, nullptr, nullptr);
-                }
-                --ahead;
             }
             mbar_drain_ring(full, n, kQdRing);
         }
@@ -645,9 +627,13 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         // warp that gave up goes on without waiting for long (the abort flag is set).
         bool bad = false;
         uint32_t nq = 0;
-        for (int n = 0; !it.done; ++n) {
+        // A piece's record is written behind the making of the next piece's query operand, whose products then run
+        // beside it.
+        int rec = -1, rec_item = 0;
+        for (int n = 0;; ++n) {
             const bool first = it.first(), last = it.last(), codes = it.codes();
-            if (it.qfirst()) {
+            if (!it.done && it.qfirst()) {
+                softmax_bar();               // qs_s is no longer read
                 // ---- the query operand: q (with QK normalisation q / rms(q) * g_q * g_k, since q_hat . k_hat =
                 // (q' . k) / rms(k)), as two e4m3 terms for codes, else in bf16.  A warp makes one head at a time, in
                 // place: the head's row of every slab is what its two 8-bit rows take.
@@ -735,6 +721,26 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 softmax_bar();               // qs_s
             }
 
+            if (rec >= 0) {
+                if (!bad) bad = !warp_wait(o_full, rec_item & 1, abort_flag);
+                tc_fence_after();
+                float* orec = p.rec_o + ((size_t)rec * 64 + h0) * kDecD + r;
+                const int hn = min(32, p.G - h0);        // heads of this half
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float o[32];
+                    tmem_ld32(tmem + lane_off + kTmO + 64 * c + h0, o);
+                    tmem_wait_ld32(o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < hn) orec[(size_t)j * kDecD + 128 * c] = o[j];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_empty);
+                rec = -1;
+            }
+            if (it.done) break;
             const int sb = n % look;
             const bool valid = r < it.nvalid();
             const uint32_t sc_next = last ? 0u : scales(it.tile + 1);      // loaded while this tile is worked on
@@ -852,10 +858,11 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             }
 
             if (last) {
-                // ---- end of this CTA's piece of unit u: the row sums over all key rows, then the
-                // record (reference, sum, unnormalised O^T)
+                // ---- end of this CTA's piece of unit u: the row sums over all key rows for its record
+                // (reference, sum, unnormalised O^T)
                 const int u = it.u;
-                const int rec = cta + u;
+                rec = cta + u;
+                rec_item = it.item;
                 const float tsum = colreduce32<false>(lsum, lane);
                 red[q4 * 64 + h0 + lane] = tsum;
                 softmax_bar();
@@ -870,22 +877,6 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 softmax_bar();     // red[] is free again before the next piece's first reduction
 #pragma unroll
                 for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
-                if (!bad) bad = !warp_wait(o_full, it.item & 1, abort_flag);
-                tc_fence_after();
-                float* orec = p.rec_o + ((size_t)rec * 64 + h0) * kDecD + r;
-                const int hn = min(32, p.G - h0);        // heads of this half
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float o[32];
-                    tmem_ld32(tmem + lane_off + kTmO + 64 * c + h0, o);
-                    tmem_wait_ld32(o);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < hn) orec[(size_t)j * kDecD + 128 * c] = o[j];
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(o_empty);
             }
             it.next();
             sc = last ? scales(it.tile) : sc_next;

@@ -1203,7 +1203,7 @@ hca_status_t attend_pass(hca::QuantParams& p, const void* q, const void* kc, con
     p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
     p.cap = paged ? (int)((long long)max_pages * page_size) : Nmax;     // checked to fit
     // the kernel counts the batch's tiles in 31 bits
-    if ((long long)B * Hkv * ((p.cap + 127LL) / 128 + 2 * ((W + 127LL) / 128)) > 0x7fffffffLL) return HCA_ERR_INVALID_ARG;
+    if ((long long)B * Hkv * ((p.cap + 127LL) / 128 + 2 * ((W + 127LL) / 128) + kQdStart) > 0x7fffffffLL) return HCA_ERR_INVALID_ARG;
     p.flags = (int)flags; p.nsplit = nsplit;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.eps = eps;
