@@ -191,7 +191,7 @@ __device__ __forceinline__ void q_range(const QuantParams& p, int cta, int grid,
     };
     int nsplit = p.nsplit;
     if (p.pfx_total > 0) {
-        const SharedPlan plan = shared_plan_warp(p.pfx_total, total, p.pfx_max, p.nsplit);
+        const SharedPlan plan = shared_plan_warp(p.pfx_total, total, U, p.pfx_max, p.nsplit);
         nsplit = min(plan.splits, grid);
         if (lane == 0 && cta == 0) *p.plan = plan;
     }

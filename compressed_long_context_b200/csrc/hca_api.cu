@@ -1085,17 +1085,22 @@ extern "C" hca_status_t hca_compress_quant(const void* k, const void* v, const f
     if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(vc) || !aligned2(scales) || (w && !aligned4(w)))
         return HCA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    using Fn = void (*)(const __nv_bfloat16*, const __nv_bfloat16*, const float*, uint8_t*, uint8_t*, uint16_t*, int, int,
+    using Fn = void (*)(const __nv_bfloat16*, const __nv_bfloat16*, const float*, uint8_t*, uint8_t*, uint8_t*, int, int,
                         int, int);
     auto index = [](int x) { return x == 64 ? 0 : x == 128 ? 1 : x == 256 ? 2 : 3; };
-#define HCA_CQ_ROW(DK)                                                            \
-    {hca::compress_quant_kernel<DK, 64>, hca::compress_quant_kernel<DK, 128>,    \
-     hca::compress_quant_kernel<DK, 256>, hca::compress_quant_kernel<DK, 512>}
-    static const Fn fns[4][4] = {HCA_CQ_ROW(64), HCA_CQ_ROW(128), HCA_CQ_ROW(256), HCA_CQ_ROW(512)};
+    // few entries (all CTAs resident at once): 512 threads have a block's rows in flight in two round trips; more
+    // entries: 256, of which more CTAs overlap
+#define HCA_CQ_ROW(DK, N)                                                               \
+    {hca::compress_quant_kernel<DK, 64, N>, hca::compress_quant_kernel<DK, 128, N>,    \
+     hca::compress_quant_kernel<DK, 256, N>, hca::compress_quant_kernel<DK, 512, N>}
+    static const Fn fns[2][4][4] = {
+        {HCA_CQ_ROW(64, 256), HCA_CQ_ROW(128, 256), HCA_CQ_ROW(256, 256), HCA_CQ_ROW(512, 256)},
+        {HCA_CQ_ROW(64, 512), HCA_CQ_ROW(128, 512), HCA_CQ_ROW(256, 512), HCA_CQ_ROW(512, 512)}};
 #undef HCA_CQ_ROW
-    fns[index(d)][index(dv)]<<<(unsigned)entries, hca::kCompressThreads, 0, s>>>(
+    const bool few = 2 * entries <= hca::num_sms();
+    fns[few][index(d)][index(dv)]<<<dim3((unsigned)entries, 2), few ? 512 : 256, 0, s>>>(
         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), w, static_cast<uint8_t*>(kc),
-        static_cast<uint8_t*>(vc), static_cast<uint16_t*>(scales), T, Hkv, blk, (int)Nc);
+        static_cast<uint8_t*>(vc), static_cast<uint8_t*>(scales), T, Hkv, blk, (int)Nc);
     return launch_status();
 }
 
@@ -1323,7 +1328,8 @@ bool shared_ws_layout(SharedWs& w, int B, int Hq, int Hkv, int Np, int nsplit) {
     return true;
 }
 
-// The prefix pass's launch over `clusters` clusters of four CTAs (attr: one element, which cfg points to).
+// The prefix pass's launch over `clusters` clusters of four CTAs (attr: two elements, which cfg points to); behind
+// prefix_prep_kernel, which it waits for itself, it may start early.
 template <bool NORM>
 bool prefix_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clusters, cudaStream_t s) {
     if (!hca::set_smem_attr_once(reinterpret_cast<const void*>(hca::prefix_kernel<NORM>), (int)hca::kPpSmem, 20 + NORM))
@@ -1332,12 +1338,14 @@ bool prefix_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int clust
     attr[0].val.clusterDim.x = 4;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(4 * (unsigned)clusters);
     cfg.blockDim = dim3(hca::kPpThreads);
     cfg.dynamicSmemBytes = hca::kPpSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = NORM ? 2 : 1;
     return true;
 }
 
@@ -1352,10 +1360,10 @@ int prefix_clusters(cudaStream_t s) {
     if (cached[dev] > 0) return cached[dev];
     const int sms = hca::num_sms();
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     int n = 0;
     if (sms < 4 || !prefix_config<NORM>(cfg, attr, sms / 4, s) ||
-        cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(hca::prefix_kernel<NORM>), &cfg) != cudaSuccess) {
+        (cfg.numAttrs = 1, cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(hca::prefix_kernel<NORM>), &cfg)) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -1367,7 +1375,7 @@ hca_status_t launch_prefix(const hca::PrefixParams& p, int clusters, const CUten
                            const CUtensorMap& tv, const CUtensorMap& tout, cudaStream_t s) {
     const auto kern = hca::prefix_kernel<NORM>;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     if (!prefix_config<NORM>(cfg, attr, clusters, s)) return HCA_ERR_CUDA;
     if (cudaLaunchKernelEx(&cfg, kern, p, tq, tk, tv, tout) != cudaSuccess) {
         cudaGetLastError();
@@ -1442,8 +1450,8 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         // that a batch of this shape can have
         const long long cap = paged ? (long long)max_pages * page_size : (long long)Nmax;
         const long long U = (long long)B * Hkv;
-        clusters = shared_plan(p.total, U, most, nsplit).clusters;
-        grid = shared_plan(p.total, U * ((cap + kDecTile - 1) / kDecTile + (W + kDecTile - 1) / kDecTile), most, nsplit).splits;
+        clusters = shared_plan(p.total, U, (int)U, most, nsplit).clusters;
+        grid = shared_plan(p.total, U * ((cap + kDecTile - 1) / kDecTile + (W + kDecTile - 1) / kDecTile), (int)U, most, nsplit).splits;
         p.max_clusters = most;
         p.sms = nsplit;
         p.cap = (int)cap;

@@ -22,26 +22,28 @@ struct SharedPlan {
     int clusters, splits;
 };
 
-// pfx: prefix tiles (256 rows x 256 keys); own: own tiles (128 keys of one sequence).  The plan with the shortest longer
-// pass, from measured times: a prefix tile takes a cluster about 2.8 us after 14 us of start and record, an own tile
-// takes one SM (its loads' latency) about 4 us after 18 us.
-__host__ __device__ inline long long shared_time(long long pfx, long long own, int c, int sms) {
+// pfx: prefix tiles (256 rows x 256 keys); own: own tiles (128 keys of one sequence) of `units` (sequence, KV head)
+// pairs.  The plan with the shortest longer pass, from measured times (tenths of a microsecond): a prefix tile takes a
+// cluster 3.1 us after 14 us of start and record; the own pass takes 10 us and 2.5 us for each tile, of which a unit's start
+// counts as two (decode_quant.cuh), in a CTA, and 6 us more where CTAs hold parts of several units.
+__host__ __device__ inline long long shared_time(long long pfx, long long own, int units, int c, int sms) {
     const int ns = sms - 4 * c;
     if (c > pfx || ns < 4) return 0x3fffffffffffffLL;
-    const long long tp = 140 + 28 * ((pfx + c - 1) / c), ts = 180 + 40 * ((own + ns - 1) / ns);
+    const long long tp = 140 + 31 * ((pfx + c - 1) / c);
+    const long long ts = 100 + 25 * ((own + 2LL * units + ns - 1) / ns) + (units > ns ? 60 : 0);
     return tp > ts ? tp : ts;
 }
-inline SharedPlan shared_plan(long long pfx, long long own, int max_clusters, int sms) {
+inline SharedPlan shared_plan(long long pfx, long long own, int units, int max_clusters, int sms) {
     int best = 1;
     for (int c = 2; c <= max_clusters; ++c)
-        if (shared_time(pfx, own, c, sms) < shared_time(pfx, own, best, sms)) best = c;
+        if (shared_time(pfx, own, units, c, sms) < shared_time(pfx, own, units, best, sms)) best = c;
     return SharedPlan{best, sms - 4 * best};
 }
 // The same by a whole warp (up to 255 clusters), on every lane.
-__device__ __forceinline__ SharedPlan shared_plan_warp(long long pfx, long long own, int max_clusters, int sms) {
+__device__ __forceinline__ SharedPlan shared_plan_warp(long long pfx, long long own, int units, int max_clusters, int sms) {
     long long key = 0x7fffffffffffffffLL;          // (time, clusters)
     for (int c = (threadIdx.x & 31) + 1; c <= max_clusters; c += 32) {
-        const long long k = shared_time(pfx, own, c, sms) << 8 | c;
+        const long long k = shared_time(pfx, own, units, c, sms) << 8 | c;
         key = k < key ? k : key;
     }
 #pragma unroll

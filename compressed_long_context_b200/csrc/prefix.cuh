@@ -101,6 +101,8 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = 2;      // rows per warp
 
 __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixPrepParams p) {
+    // the prefix pass may set itself up meanwhile; it waits for this grid before it reads the rows
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const long long i0 = ((long long)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5)) * kPrepRows;
     uint4 x[kPrepRows][2];
@@ -286,7 +288,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
         for (int b = lane; b < p.B; b += 32) own += own_tiles(__ldg(p.seqlens + b), p.W, p.blk, p.Np, p.cap);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) own += __shfl_xor_sync(0xffffffffu, own, off);
-        const SharedPlan plan = shared_plan_warp(p.total, own * p.Hkv, p.max_clusters, p.sms);
+        const SharedPlan plan = shared_plan_warp(p.total, own * p.Hkv, p.B * p.Hkv, p.max_clusters, p.sms);
         if (lane == 0) misc[3] = min((int)(gridDim.x >> 2), plan.clusters);
     }
     tc_fence_before();
@@ -300,6 +302,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
     bool go = true;
     for (uint32_t c = 0; c < 4; ++c) go &= pp_ld_cluster_u32(pp_mapa(smem_u32(misc + 2), c)) != 0;
     if (!go && threadIdx.x == 0) record_error(HCA_ERR_INTERNAL);
+    if (NORM) asm volatile("griddepcontrol.wait;" ::: "memory");       // prefix_prep_kernel's rows
     const int cl = blockIdx.x >> 2;               // this cluster's range of the list of (row tile, key tile)
     const long long per = pfx_per(p.total, misc[3]);
     const long long x_beg = min(p.total, cl * per), x_end = min(p.total, x_beg + per);

@@ -52,30 +52,42 @@ __device__ __forceinline__ void block_alpha(const float* __restrict__ w, int64_t
         if (lane + 32 * i < blk) alpha[lane + 32 * i] = wv[i] * inv;
 }
 
-// Weighted sum over `blk` rows of one tensor with D channels, then the codes of the pooled vector.
-// Returns the scale byte.
-template <int D>
-__device__ __forceinline__ uint32_t pool_rows_quant(const __nv_bfloat16* __restrict__ src, int64_t row_stride,
-                                                    const float* __restrict__ alpha, int blk,
-                                                    float* __restrict__ red, float* __restrict__ scratch,
-                                                    uint8_t* __restrict__ dst) {
+constexpr int kPoolUnroll = 8;
+
+// One CTA per (entry, tensor): the weighted sum over `blk` rows of D channels, then the codes of the pooled vector and its
+// scale.  A stream over memory: 64 KB in flight per CTA (a lone entry takes two round trips), the first rows
+// requested before the weights' softmax, whose latency they cover.  K and V of an entry are separate CTAs: few entries
+// fill twice the SMs.
+template <int D, int THREADS>
+__device__ __forceinline__ void pool_rows_quant(const __nv_bfloat16* __restrict__ src, int64_t row_stride,
+                                                const float* __restrict__ w, int64_t pos0, int blk,
+                                                float* __restrict__ alpha, float* __restrict__ red,
+                                                float* __restrict__ scratch, uint8_t* __restrict__ dst,
+                                                uint8_t* __restrict__ scale) {
     constexpr int TPR = D / 8;                   // threads per row (16 bytes each)
-    constexpr int R = kCompressThreads / TPR;    // rows in flight per pass
+    constexpr int R = THREADS / TPR;        // rows in flight per pass
     const int tid = threadIdx.x;
     const int c0 = (tid % TPR) * 8;
     const int r0 = tid / TPR;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int r = r0; r < blk; r += R * kCompressUnroll) {
-        uint4 x[kCompressUnroll];
+    const __nv_bfloat16* at = src + r0 * row_stride + c0;
+    const int64_t step = R * row_stride;
+    for (int r = r0; r - r0 < blk; r += R * kPoolUnroll) {      // the same passes for every thread
+        uint4 x[kPoolUnroll];
 #pragma unroll
-        for (int u = 0; u < kCompressUnroll; ++u) {
+        for (int u = 0; u < kPoolUnroll; ++u) {
             const int rr = r + u * R;
-            if (rr < blk) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + rr * row_stride + c0));
+            if (rr < blk) x[u] = __ldcs(reinterpret_cast<const uint4*>(at));
+            at += step;
+        }
+        if (r == r0) {
+            if (tid < 32) block_alpha(w, pos0, blk, alpha);
+            __syncthreads();
         }
 #pragma unroll
-        for (int u = 0; u < kCompressUnroll; ++u) {
+        for (int u = 0; u < kPoolUnroll; ++u) {
             const int rr = r + u * R;
             if (rr < blk) {
                 const float a = alpha[rr];
@@ -90,49 +102,53 @@ __device__ __forceinline__ uint32_t pool_rows_quant(const __nv_bfloat16* __restr
             }
         }
     }
-    float4* o = reinterpret_cast<float4*>(red + r0 * D + c0);
-    o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    // rows of one warp first (narrow rows: several to a warp), then across warps
+    constexpr int RW = TPR < 32 ? 32 / TPR : 1;
+#pragma unroll
+    for (int off = TPR; off < 32; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
+    if (r0 % RW == 0) {
+        float4* o = reinterpret_cast<float4*>(red + (r0 / RW) * D + c0);
+        o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
     __syncthreads();
-    // two channels per thread; D / 2 <= kCompressThreads
+    // two channels per thread
     float s0 = 0.f, s1 = 0.f;
     const bool mine = tid < D / 2;
     if (mine) {
-#pragma unroll 4
-        for (int r = 0; r < R; ++r) {
+#pragma unroll 8
+        for (int r = 0; r < R / RW; ++r) {
             const float2 p = *reinterpret_cast<const float2*>(red + r * D + 2 * tid);
             s0 += p.x;
             s1 += p.y;
         }
     }
-    const uint32_t byte = q_scale_byte(block_amax<kCompressThreads>(fmaxf(q_mag(s0), q_mag(s1)), scratch));
+    const uint32_t byte = q_scale_byte(block_amax<THREADS>(fmaxf(q_mag(s0), q_mag(s1)), scratch));
     const float inv = q_inv_scale(byte);
     if (mine) reinterpret_cast<uint16_t*>(dst)[tid] = (uint16_t)cvt_e4m3x2(q_prep(s0, inv), q_prep(s1, inv));
-    __syncthreads();
-    return byte;
+    if (tid == 0) *scale = (uint8_t)byte;
 }
 
-template <int DK, int DV>
-__global__ void __launch_bounds__(kCompressThreads)
+template <int DK, int DV, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS)
 compress_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                       const float* __restrict__ w, uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
-                      uint16_t* __restrict__ sc, int T, int Hkv, int blk, int Nc) {
+                      uint8_t* __restrict__ sc, int T, int Hkv, int blk, int Nc) {
     __shared__ float alpha[128];
-    __shared__ __align__(16) float red[kCompressThreads * 8];
-    __shared__ float scratch[kCompressThreads / 32];
+    __shared__ __align__(16) float red[THREADS * 8];
+    __shared__ float scratch[THREADS / 32];
     const int e = blockIdx.x;                 // entry index, KV head fastest
-    const int g = e % Hkv;
-    const int bj = e / Hkv;
-    const int j = bj % Nc;
-    const int b = bj / Nc;
+    const int bj = e / Hkv, g = e - bj * Hkv;
+    const int b = bj / Nc, j = bj - b * Nc;
     const int64_t pos0 = (int64_t)b * T + (int64_t)blk * j;
-    if (threadIdx.x < 32) block_alpha(w, pos0, blk, alpha);
-    __syncthreads();
-    const uint32_t kb = pool_rows_quant<DK>(k + (pos0 * Hkv + g) * DK, (int64_t)Hkv * DK, alpha, blk, red, scratch,
-                                            kc + (int64_t)e * DK);
-    const uint32_t vb = pool_rows_quant<DV>(v + (pos0 * Hkv + g) * DV, (int64_t)Hkv * DV, alpha, blk, red, scratch,
-                                            vc + (int64_t)e * DV);
-    if (threadIdx.x == 0) sc[e] = (uint16_t)(kb | vb << 8);
+    if (blockIdx.y == 0)
+        pool_rows_quant<DK, THREADS>(k + (pos0 * Hkv + g) * DK, (int64_t)Hkv * DK, w, pos0, blk, alpha, red, scratch,
+                            kc + (int64_t)e * DK, sc + 2 * (int64_t)e);
+    else
+        pool_rows_quant<DV, THREADS>(v + (pos0 * Hkv + g) * DV, (int64_t)Hkv * DV, w, pos0, blk, alpha, red, scratch,
+                            vc + (int64_t)e * DV, sc + 2 * (int64_t)e + 1);
 }
 
 // ------------------------------------------------------------------ append
@@ -284,8 +300,8 @@ __global__ void __launch_bounds__(kReadThreads) read_quant_kernel(const ReadQuan
                     y[2 * q + 1] = pack_bf16x2(b2.x * s, b2.y * s);
                 }
                 uint4* o = reinterpret_cast<uint4*>(dst + c);
-                o[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                __stcs(o, make_uint4(y[0], y[1], y[2], y[3]));
+                __stcs(o + 1, make_uint4(y[4], y[5], y[6], y[7]));
             }
         };
         widen(p.kc + rg * p.d, p.k + (size_t)i * p.d, p.d, q_scale(sc & 0xffu));
