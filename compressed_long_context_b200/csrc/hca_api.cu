@@ -1048,7 +1048,7 @@ hca_status_t launch_merge(const hca::MergeParams& mp, bool prefix, cudaStream_t 
     const long long U = (long long)mp.B * mp.Hkv;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)U, (unsigned)(kDecD / kMergeCh));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = mp.vha_u ? combine_vha_smem(mp.vha_r) : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

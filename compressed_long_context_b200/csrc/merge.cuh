@@ -6,8 +6,8 @@
 // 2^(z - m) and the 512 sums of 2^(z - m) v.  hca_decode_shared adds a second kind: the shared prefix
 // of 2 * (128 / G) sequences at once.
 //
-// Grid (units, 512 / 32), 128 threads: a CTA owns all G heads of one unit for 32 channels, so the mixing across
-// heads stays on chip.  Thread = (4 channels, heads hb, hb + 16, hb + 32, hb + 48): a warp reads whole 128-byte
+// Grid (units, 512 / 32), 256 threads: a CTA owns all G heads of one unit for 32 channels, so the mixing across
+// heads stays on chip.  Thread = (4 channels, heads hb, hb + 32): a warp reads whole 128-byte
 // lines of four heads.  The records of a chunk are all loaded before any is used (one memory round trip for up to
 // kChunk of them).
 #pragma once
@@ -79,10 +79,12 @@ struct MergeParams {
     const SharedPlan* plan;
 };
 
-constexpr int kMergeHeads = 4;            // heads per thread
+constexpr int kMergeHeads = 2;            // heads per thread
+constexpr int kMergeThreads = 256;
+constexpr int kMergeStep = kMergeThreads / 8;    // a thread's heads are this far apart
 
 template <int kChunk, bool kVha, bool kPfx>
-__global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
     extern __shared__ float cs[];
     const int u = blockIdx.x;
     const int hb = threadIdx.x >> 3;
@@ -100,18 +102,22 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
 #pragma unroll
     for (int x = 0; x < kMergeHeads; ++x) {
         graw[x] = make_uint2(0, 0);
-        if (p.gate && hb + 16 * x < p.G) graw[x] = __ldg(reinterpret_cast<const uint2*>(p.gate + orow + (size_t)16 * x * kDecD));
+        if (p.gate && hb + kMergeStep * x < p.G) graw[x] = __ldg(reinterpret_cast<const uint2*>(p.gate + orow + (size_t)kMergeStep * x * kDecD));
     }
     const int len = __ldg(p.seqlens + b);
     if (kVha) {
-        for (int i = threadIdx.x; i < p.G * R; i += 128) {
+        for (int i = threadIdx.x; i < p.G * R; i += kMergeThreads) {
             vs[i] = __ldg(p.vha_v + i);
             us[i] = __ldg(p.vha_u + i);
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float4 r[kMergeHeads];
-    if (*reinterpret_cast<volatile unsigned int*>(&g_error) == HCA_ERR_TIMEOUT) {
+    // requested together: a second round trip then brings the records
+    const unsigned err = __ldcg(&g_error);
+    const int first = __ldcg(p.meta + 2 * u), last = __ldcg(p.meta + 2 * u + 1);
+    const int clusters = kPfx ? __ldcg(&p.plan->clusters) : 0;
+    if (err == HCA_ERR_TIMEOUT) {
         // a CTA gave up: its records may be stale, so the outputs are marked invalid
 #pragma unroll
         for (int x = 0; x < kMergeHeads; ++x) r[x] = make_float4(NAN, NAN, NAN, NAN);
@@ -138,8 +144,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
 #pragma unroll
                     for (int x = 0; x < kMergeHeads; ++x) {
                         // ranges are contiguous: every record is there
-                        const bool ok = hb + 16 * x < p.G && i0 + k <= last;
-                        const size_t rec = (rec0 + (size_t)(i0 + k)) * stride + row + hb + 16 * x;
+                        const bool ok = hb + kMergeStep * x < p.G && i0 + k <= last;
+                        const size_t rec = (rec0 + (size_t)(i0 + k)) * stride + row + hb + kMergeStep * x;
                         m[k][x] = ok ? __ldcg(pm + rec) : -INFINITY;
                         l[k][x] = ok ? __ldcg(pl + rec) : 0.f;
                         o[k][x] = ok ? __ldcg(reinterpret_cast<const float4*>(po + rec * kDecD + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -168,7 +174,6 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
                 }
             }
         };
-        const int first = __ldcg(p.meta + 2 * u), last = __ldcg(p.meta + 2 * u + 1);
         if (first < 0 || last < first || last >= p.nsplit) {
             if (threadIdx.x == 0 && blockIdx.y == 0) record_error(HCA_ERR_DEVICE_INPUT);
         } else {
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
         }
         if (kPfx && p.pfx_tiles > 0) {
             const int rt = (b / (2 * p.tpt)) * p.Hkv + g;
-            const long long per = pfx_per(p.pfx_total, min(__ldcg(&p.plan->clusters), p.pfx_clusters));
+            const long long per = pfx_per(p.pfx_total, min(clusters, p.pfx_clusters));
             const int pf = (int)((long long)rt * p.pfx_tiles / per);
             const int pl = (int)(((long long)(rt + 1) * p.pfx_tiles - 1) / per);
             fold(p.pfx_m, p.pfx_l, p.pfx_o, pf, pl, (size_t)rt, (b / p.tpt & 1) * 128 + (b % p.tpt) * p.G, 256);
@@ -197,9 +202,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
         // o'[:, ch] = o[:, ch] + U (V^T o[:, ch]) over the G heads of this token (see decode.cuh)
 #pragma unroll
         for (int x = 0; x < kMergeHeads; ++x)
-            if (hb + 16 * x < p.G) *reinterpret_cast<float4*>(os + (hb + 16 * x) * kMergeCh + c4) = r[x];
+            if (hb + kMergeStep * x < p.G) *reinterpret_cast<float4*>(os + (hb + kMergeStep * x) * kMergeCh + c4) = r[x];
         __syncthreads();
-        for (int i = threadIdx.x; i < R * (kMergeCh / 4); i += 128) {
+        for (int i = threadIdx.x; i < R * (kMergeCh / 4); i += kMergeThreads) {
             const int k = i >> 3, cc = (i & 7) * 4;
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -218,8 +223,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
             const float4 t4 = *reinterpret_cast<const float4*>(ts + k * kMergeCh + c4);
 #pragma unroll
             for (int x = 0; x < kMergeHeads; ++x) {
-                if (hb + 16 * x >= p.G) continue;
-                const float uk = us[(hb + 16 * x) * R + k];
+                if (hb + kMergeStep * x >= p.G) continue;
+                const float uk = us[(hb + kMergeStep * x) * R + k];
                 r[x].x = fmaf(uk, t4.x, r[x].x);
                 r[x].y = fmaf(uk, t4.y, r[x].y);
                 r[x].z = fmaf(uk, t4.z, r[x].z);
@@ -229,8 +234,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
     }
 #pragma unroll
     for (int x = 0; x < kMergeHeads; ++x) {
-        if (hb + 16 * x >= p.G) continue;
-        const size_t at = orow + (size_t)16 * x * kDecD;
+        if (hb + kMergeStep * x >= p.G) continue;
+        const size_t at = orow + (size_t)kMergeStep * x * kDecD;
         if (p.out_f32)
             *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = r[x];
         else
