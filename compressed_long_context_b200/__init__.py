@@ -475,11 +475,11 @@ def compress_quant(k, v, w=None, blk=128, kc=None, vc=None, sc=None):
     Nc = T // blk if blk > 0 else 0
     n = B * Nc * Hkv
     if kc is None:
-        kc = torch.empty((B, Nc, Hkv, d), dtype=_E4M3, device=dev)
+        kc = k.new_empty((B, Nc, Hkv, d), dtype=_E4M3)
     if vc is None:
-        vc = torch.empty_like(kc) if d == dv else torch.empty((B, Nc, Hkv, dv), dtype=_E4M3, device=dev)
+        vc = torch.empty_like(kc) if d == dv else k.new_empty((B, Nc, Hkv, dv), dtype=_E4M3)
     if sc is None:
-        sc = torch.empty((B, Nc, Hkv, 2), dtype=_E8M0, device=dev)
+        sc = k.new_empty((B, Nc, Hkv, 2), dtype=_E8M0)
     _all(dev, (v, _BF16, B * T * Hkv * dv, "v"), (kc, _E4M3, n * d, "kc"), (vc, _E4M3, n * dv, "vc"),
          (sc, _scale_type(sc), 2 * n, "sc"))
     if w is not None:
@@ -581,7 +581,7 @@ def decode_quant(q, kc, vc, sc, kw, vw, seqlens, blk, W, scale, page_table=None,
          (kw, _BF16, B * W * Hkv * d, "kw"), (vw, _BF16, B * W * Hkv * dv, "vw"), (seqlens, _I32, B, "seqlens"))
     f, out, r = _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q)
     if workspace is None:
-        workspace = torch.empty(_ws_size(decode_workspace_size, dev, B, Hq, Hkv, dv), dtype=_U8, device=dev)
+        workspace = q.new_empty(_ws_size(decode_workspace_size, dev, B, Hq, Hkv, dv), dtype=_U8)
     else:
         _all(dev, (workspace, _U8, 0, "workspace"))
     _run("hca_decode_quant", dev, _p(q), _p(kc), _p(vc), _p(sc), _p(page_table), page_size, max_pages, num_pages, _p(kw),
@@ -611,7 +611,7 @@ def decode_shared(q, kp, vp, kc, vc, kw, vw, seqlens, blk, W, scale, page_table=
          (seqlens, _I32, B, "seqlens"))
     f, out, r = _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q)
     if workspace is None:
-        workspace = torch.empty(_ws_size(decode_shared_workspace_size, dev, B, Hq, Hkv, dv, Np), dtype=_U8, device=dev)
+        workspace = q.new_empty(_ws_size(decode_shared_workspace_size, dev, B, Hq, Hkv, dv, Np), dtype=_U8)
     else:
         _all(dev, (workspace, _U8, 0, "workspace"))
     _run("hca_decode_shared", dev, _p(q), _p(kp), _p(vp), _p(kc), _p(vc), _p(page_table), page_size, max_pages, num_pages,
