@@ -469,3 +469,135 @@ def test_pipeline_streams_graph(cuda_device, libhca):
     done()
     for x, y in zip(a, b):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_decode_device_input_errors(cuda_device, libhca):
+    """A length past the cache, a negative one and a page outside the pool are reported, not followed."""
+    args, _, _ = decode_case(cuda_device, 3, [16 * 300 + 50, 900], 64, 1, 16, 40, ps=64)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    for bad in (dict(seqlens=i32(1 << 30, 900)), dict(seqlens=i32(-5, 900)),
+                dict(page_table=torch.full_like(args["page_table"], 1 << 20)),
+                dict(page_table=torch.full_like(args["page_table"], -1))):
+        hca.decode_quant(**{**args, **bad})
+        with pytest.raises(hca.HCAError) as e:
+            hca.get_device_error()
+        assert e.value.code == 5
+        hca.get_device_error()
+
+
+@pytest.mark.gpu
+def test_decode_large_batch(cuda_device, libhca):
+    """More units than CTAs, and than tile counts are kept on chip: every row equals its own small batch's."""
+    dev, g = cuda_device, torch.Generator(device=cuda_device).manual_seed(2)
+    B, N, W = 2500, 9, 5
+    kc, ks, _ = rand_cache(g, dev, (B, N, 1, 512))
+    vc, vs, _ = rand_cache(g, dev, (B, N, 1, 512))
+    sc = pair(ks, vs)
+    q, kw, vw = (torch.randn(s, generator=g, device=dev).to(bf) for s in ((B, 4, 512), (B, W, 1, 512), (B, W, 1, 512)))
+    seq = torch.randint(0, 16 * N + W + 16, (B,), generator=g, device=dev).to(torch.int32)
+    a = lambda s: (q[s], kc[s], vc[s], sc[s], kw[s], vw[s], seq[s])  # noqa: E731
+    big = hca.decode_quant(*a(slice(None)), 16, W, 0.05, out_f32=True)
+    for b in (0, 1, 1023, 2047, 2048, 2300, 2499):
+        one = hca.decode_quant(*a(slice(b, b + 1)), 16, W, 0.05, out_f32=True)
+        done()
+        assert torch.allclose(big[b], one[0], rtol=2e-6, atol=1e-6)     # (fp32 merge in another order)
+
+
+@pytest.mark.gpu
+def test_decode_two_streams(cuda_device, libhca):
+    """Two calls at once, each with its own workspace."""
+    cases = [decode_case(cuda_device, s, [16 * 700 + 50, 16 * 90], 64, 1, 16, 40, norm=s == 1) for s in range(2)]
+    want = [hca.decode_quant(**c[0]) for c in cases]
+    done()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(hca.decode_quant(**cases[i][0]))
+    done()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)
+
+
+@pytest.mark.gpu
+def test_decode_unwinds_after_a_missing_slab(cuda_device, libhca):
+    """A wait that runs out (shortened, on a key slab that is never requested) is reported and marks the output."""
+    stream = torch.cuda.current_stream().cuda_stream
+    args, out, tol = decode_case(cuda_device, 3, [16 * 300 + 50, 900], 64, 1, 16, 40)
+    hca.get_device_error()
+    try:
+        assert libhca.hca_debug_set_wait_limit(2_000_000, stream) == _lib.HCA_OK      # 2 ms
+        assert libhca.hca_debug_set_drop_slab(1, stream) == _lib.HCA_OK
+        bad = hca.decode_quant(**args)
+        torch.cuda.synchronize()
+        assert libhca.hca_get_device_error(stream) == _lib.HCA_ERR_TIMEOUT
+        assert torch.isnan(bad).all()
+    finally:
+        libhca.hca_debug_set_drop_slab(0, stream)
+        libhca.hca_debug_set_wait_limit(0, stream)
+    hca.get_device_error()
+    good = hca.decode_quant(**args)
+    done()
+    check(good, out, tol)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(cuda_device, libhca):
+    """A pool of more than 2^32 code bytes, used at its end: the same bits as from a small pool."""
+    dev = cuda_device
+    args, _, _ = decode_case(dev, 6, [16 * 200 + 45], 64, 1, 16, 40, ps=64)
+    P = (1 << 32) // (64 * 512) + 100
+    move = lambda t: t + (P - 1 - int(args["page_table"].max()))  # noqa: E731
+    pools = {}
+    for name in ("kc", "vc", "sc"):
+        small = args[name]
+        big = torch.empty((P,) + small.shape[1:], dtype=torch.uint8, device=dev).view(small.dtype)
+        big.view(torch.uint8)[P - small.shape[0]:] = 0
+        for i in args["page_table"].flatten().tolist():
+            big.view(torch.uint8)[int(move(i))] = small.view(torch.uint8)[i]
+        pools[name] = big
+    table = move(args["page_table"])
+    want, got = hca.decode_quant(**args), hca.decode_quant(**{**args, **pools, "page_table": table})
+    cnt = torch.tensor([200], dtype=torch.int32, device=dev)
+    rw = hca.read_quant(args["kc"], args["vc"], args["sc"], cnt, 200, page_table=args["page_table"])
+    rg = hca.read_quant(pools["kc"], pools["vc"], pools["sc"], cnt, 200, page_table=table)
+    # and an entry written there
+    g = torch.Generator(device=dev).manual_seed(1)
+    kn, vn = (torch.randn(1, 1, 512, generator=g, device=dev).to(bf) for _ in range(2))
+    kw = torch.zeros(1, 8, 1, 512, dtype=bf, device=dev)
+    outs = []
+    for kc, vc, sc, t in ((args["kc"], args["vc"], args["sc"], args["page_table"]), (pools["kc"], pools["vc"], pools["sc"], table)):
+        st = torch.zeros(hca.append_state_size(1, 1, 512, 512), dtype=torch.uint8, device=dev)
+        hca.append_quant(kn, vn, None, torch.tensor([131], dtype=torch.int32, device=dev), kw, kw.clone(), kc, vc, sc, st, 1,
+                         page_table=t)
+        pg = int(t[0, 130 // 64])
+        outs.append([x.view(torch.uint8)[pg, 130 % 64] for x in (kc, vc, sc)])
+    done()
+    assert torch.equal(want, got) and all(torch.equal(a, b) for a, b in zip(rw, rg))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and torch.equal(outs[0][0].view(f8)[0].float().nan_to_num().ne(0),
+                                                                         outs[1][0].view(f8)[0].float().nan_to_num().ne(0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 3])
+def test_write_no_entries(cuda_device, libhca, n):
+    """Fewer tokens than a block: nothing to write, empty results."""
+    k = torch.ones(2, n, 1, 64, dtype=bf, device=cuda_device)
+    kc, vc, sc = hca.compress_quant(k, k, blk=4)
+    done()
+    assert kc.shape == (2, 0, 1, 64) and sc.shape == (2, 0, 1, 2)
+
+
+@pytest.mark.gpu
+def test_decode_not_finite_query(cuda_device, libhca):
+    """NaN or infinity in one head's query stays in that head."""
+    args, out, tol = decode_case(cuda_device, 3, [16 * 300 + 50], 64, 1, 16, 40)
+    q = args["q"].clone()
+    q[0, 5, 100], q[0, 9, 3] = float("nan"), float("inf")
+    got = hca.decode_quant(**{**args, "q": q})
+    done()
+    rest = [h for h in range(64) if h not in (5, 9)]
+    assert torch.isnan(got[0, 5]).all() and torch.isnan(got[0, 9]).all()
+    check(got[:, rest], out[:, rest], tol[:, rest])

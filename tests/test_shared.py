@@ -214,3 +214,66 @@ def test_device_input_errors(cuda_device, libhca):
             hca.get_device_error()
         assert e.value.code == 5
         hca.get_device_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_large_batch(cuda_device, libhca, norm):
+    """Many row tiles and more units than CTAs: rows equal their own small batch's (fp32 sums in another order, and
+    bf16 probabilities against another reference: 2^-8 of the mass at most, here against the formula's bound)."""
+    L = [16 * 320 + 60 + 5 * i for i in range(300)]
+    args, out, tol = make(cuda_device, 3, L, 310, 8, 1, 16, 50, norm=norm)
+    got = hca.decode_shared(**args, out_f32=True)
+    done()
+    check(got, out, tol, 2.0 ** -16)
+
+
+@pytest.mark.gpu
+def test_two_streams(cuda_device, libhca):
+    """Two calls at once, each with its own workspace, and one workspace used again."""
+    cases = [make(cuda_device, s, [16 * 700 + 50 + i for i in range(5)], 600, 64, 1, 16, 40, norm=s == 1) for s in range(2)]
+    want = [hca.decode_shared(**c[0]) for c in cases]
+    ws = torch.empty(hca.decode_shared_workspace_size(5, 64, 1, 512, 600), dtype=torch.uint8, device=cuda_device)
+    again = [hca.decode_shared(**c[0], workspace=ws) for c in cases]
+    done()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(hca.decode_shared(**cases[i][0]))
+    done()
+    for g, w, a in zip(got, want, again):
+        assert torch.equal(a, w) and all(torch.equal(x, w) for x in g)
+
+
+@pytest.mark.gpu
+def test_short_workspace_is_refused(cuda_device, libhca):
+    args, _, _ = make(cuda_device, 4, [16 * 30 + 60], 20, 64, 1, 16, 50)
+    n = hca.decode_shared_workspace_size(1, 64, 1, 512, 20)
+    with pytest.raises(hca.HCAError) as e:
+        hca.decode_shared(**args, workspace=torch.empty(n - 256, dtype=torch.uint8, device=cuda_device))
+    assert e.value.code == _lib.HCA_ERR_INVALID_ARG
+    done()
+
+
+@pytest.mark.gpu
+def test_unwinds_after_a_missing_slab(cuda_device, libhca):
+    """A wait that runs out in the own pass is reported and marks the output; the next call is right."""
+    stream = torch.cuda.current_stream().cuda_stream
+    args, out, tol = make(cuda_device, 4, [16 * 400 + 60 + i for i in range(7)], 390, 64, 1, 16, 50)
+    hca.get_device_error()
+    try:
+        assert libhca.hca_debug_set_wait_limit(2_000_000, stream) == _lib.HCA_OK      # 2 ms
+        assert libhca.hca_debug_set_drop_slab(1, stream) == _lib.HCA_OK
+        bad = hca.decode_shared(**args)
+        torch.cuda.synchronize()
+        assert libhca.hca_get_device_error(stream) == _lib.HCA_ERR_TIMEOUT
+        assert torch.isnan(bad).all()
+    finally:
+        libhca.hca_debug_set_drop_slab(0, stream)
+        libhca.hca_debug_set_wait_limit(0, stream)
+    hca.get_device_error()
+    good = hca.decode_shared(**args)
+    done()
+    check(good, out, tol)
