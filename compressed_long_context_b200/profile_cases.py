@@ -9,6 +9,8 @@
     python -m compressed_long_context_b200.profile_cases gate     [--reps N]
     python -m compressed_long_context_b200.profile_cases backward [--reps N] [--T tokens]
     python -m compressed_long_context_b200.profile_cases dsa      [--reps N]   (index + topk + attend)
+    python -m compressed_long_context_b200.profile_cases compress_quant | read_quant | decode_quant [--reps N]
+    python -m compressed_long_context_b200.profile_cases shared   [--reps N]   (prefix + own tiles + merge)
 
 Each case keeps its working set larger than the 126 MB L2 (so DRAM counters mean
 something) but a few GB at most, and launches the kernel `--reps` times after one
@@ -22,8 +24,9 @@ import math
 
 import torch
 
-from . import (append, append_state_size, compress, decode, decode_workspace_size, dsa_attend, dsa_index, dsa_topk,
-               gate_logits, get_device_error, prefill, prefill_backward, vha)
+from . import (append, append_state_size, compress, compress_quant, decode, decode_quant, decode_shared,
+               decode_workspace_size, dsa_attend, dsa_index, dsa_topk, gate_logits, get_device_error, prefill,
+               prefill_backward, read_quant, vha)
 from . import workloads as wl
 
 
@@ -147,6 +150,43 @@ def run(case: str, reps: int, B_override: int = 0, L_override: int = 0, T_overri
             dsa_topk(scores, inp["seqlens"], cfg.topk, idx=idx)
             dsa_attend(inp["q"], inp["k"], inp["v"], idx, inp["seqlens"], 1 / math.sqrt(cfg.d), out=out)
         nbytes = cfg.B * cfg.L * (cfg.dI * 2 + 8) + cfg.B * cfg.topk * (4 * cfg.d + 8)
+    elif case in ("compress_quant", "read_quant", "decode_quant"):
+        # 2 sequences x 131072 tokens pooled into 8-bit entries; 64 sequences of 128K tokens read back and decoded
+        d, W = 512, 128
+        if case == "compress_quant":
+            B, T = 2, 131072
+            k, v = (torch.randn((B, T, 1, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+            w = torch.randn((B, T), generator=g, device=dev) * 0.5
+            o = compress_quant(k, v, w, 128)
+            fn = lambda: compress_quant(k, v, w, 128, kc=o[0], vc=o[1], sc=o[2])  # noqa: E731
+            nbytes = B * T * (4 * d + 4) + B * (T // 128) * (2 * d + 2)
+        else:
+            B, N = 256, 1023
+            raw = torch.randn((B, N, 1, 2 * d), generator=g, device=dev) * 40
+            kc, vc = (raw[..., i * d:(i + 1) * d].to(torch.float8_e4m3fn).contiguous() for i in range(2))
+            del raw
+            sc = torch.full((B, N, 1, 2), 121, dtype=torch.uint8, device=dev)
+            if case == "read_quant":
+                cnt = torch.full((B,), N, dtype=torch.int32, device=dev)
+                ko, vo = (torch.empty((B, N, 1, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+                fn = lambda: read_quant(kc, vc, sc, cnt, N, k_out=ko, v_out=vo)  # noqa: E731
+                nbytes = B * N * (2 * d + 2 + 4 * d)
+            else:
+                q = torch.randn((B, 64, d), generator=g, device=dev).to(torch.bfloat16)
+                kw, vw = (torch.randn((B, W, 1, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+                seq = torch.full((B,), 131072, dtype=torch.int32, device=dev)
+                fn = lambda: decode_quant(q, kc, vc, sc, kw, vw, seq, 128, W, d ** -0.5)  # noqa: E731
+                nbytes = B * (1022 * (2 * d + 2) + W * 4 * d + 64 * d * 4)
+    elif case == "shared":
+        # 64 sequences of up to 16 entries of their own on one prefix of 8191 entries
+        B, Np, d, W = 64, 8191, 512, 128
+        q = torch.randn((B, 64, d), generator=g, device=dev).to(torch.bfloat16)
+        kp, vp = (torch.randn((Np, 1, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+        kc, vc = (torch.randn((B, 16, 1, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+        kw, vw = (torch.randn((B, W, 1, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+        seq = torch.full((B,), (Np + 16) * 128 + W, dtype=torch.int32, device=dev)
+        fn = lambda: decode_shared(q, kp, vp, kc, vc, kw, vw, seq, 128, W, d ** -0.5)  # noqa: E731
+        nbytes = 2048 * (Np + B * (16 + W)) + B * 64 * d * 4
     else:
         raise ValueError(case)
     _last_fn[0] = fn
@@ -199,7 +239,8 @@ def run_flushed(args) -> dict:
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["compress", "decode", "paged", "prefill", "vha", "append", "gate", "backward", "dsa"])
+    ap.add_argument("case", choices=["compress", "decode", "paged", "prefill", "vha", "append", "gate", "backward", "dsa",
+                                       "compress_quant", "read_quant", "decode_quant", "shared"])
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--B", type=int, default=0, help="decode batch (default 64)")
     ap.add_argument("--L", type=int, default=0, help="decode context length (default 131072)")
