@@ -11,15 +11,15 @@
 //       significant bits and lo the next 4: a bf16 query (8 bits) is represented exactly down to 2^-10 of its
 //       head's largest channel, and to 2^-18.8 of that channel below.  Same rounding (2^-8 at most) as bf16
 //       for the fp32 queries that QK normalisation makes.
-//   p = hi (e4m3) + lo (e5m2): where hi is normal (p >= 2^-6, 2^-12 of the row's largest) at most 2^-4 * 2^-3 =
+//   p = hi (e4m3) + lo (e5m2): where hi is normal (p >= 2^-6, 2^-10 of the row's largest) at most 2^-4 * 2^-3 =
 //       2^-7 off, 2^-10 in the mean square; below, hi is within 2^-10 and lo within 2^-3 of the rest: 2^-13, or
-//       2^-19 of the largest.  lo is e5m2 because its range matters more than its last bit: a probability down to
-//       2^-22 of the largest still has a term, so a long tail of small probabilities is kept.
+//       2^-17 of the largest.  lo is e5m2 because its range matters more than its last bit: a probability down to
+//       2^-20 of the largest still has a term, so a long tail of small probabilities is kept.
 // The scale of a value vector belongs to the key, which is the contraction's axis, so it goes into p: with
 // y = z + log2(vscale), the accumulators hold sums of 2^(y - m) * code, the reference m is the running
-// maximum of y, and the row sum l adds 2^(y - m) / vscale = 2^(z - m).  m is kept 2^6 below the maximum
-// and moves when some y exceeds it by 2^8, so that p <= 256 and 2^6 for the largest key: e4m3 ends at 448.
-//
+// maximum of y, and the row sum l adds 2^(y - m) / vscale = 2^(z - m).  m is kept 2^4 below the maximum
+// and moves when some y exceeds it by 2^8, so that p <= 256 and 2^4 for the largest key: e4m3 ends at 448.  (2^6
+// moved it, and with it 64 KB of accumulators, in most tiles of the ragged batch: 166 us, 2^4: 159.)
 // The same kernel with bf16 entries (E8 = false) attends what the sequences of hca_decode_shared do not have in
 // common: then all tiles are of the window's kind, and the reference moves at 2^32 (bf16 holds any p).
 //
@@ -31,9 +31,14 @@
 //   warp 2      the CTA's range of tiles, then tcgen05.mma  O^T[512 x 64] += V^T P^T over the 32-key (bf16: 16-key)
 //               steps that hold a key;
 //   warps 4-11  softmax, two per TMEM lane quarter, thread = (key row, 32 heads); record at a piece's end.
-// What bounds a small call is its chain of first steps, whose code is fetched cold (about 30 cycles an
-// instruction): they are loops, not unrolled, the range is found by one warp, and the MMA issuers are elected.
-// One 4K sequence (one tile of each kind on two CTAs): 27 -> see the figures at the end of this comment.
+//
+// What bounds it.  A small call: its chain of first steps, whose code is fetched cold (about 30 cycles an instruction).
+// So they are loops, not unrolled, the range is found by one warp, and the MMA issuers are elected: one 4K sequence
+// (one tile of each kind on two CTAs) takes 17.3 us with the merge, where unrolled set-up code and issuers chosen by
+// lane took 27.  A large one: the chain softmax - PV - reference of a tile (3 us, of which the MMAs take 1.6, bound by
+// the shared memory that they read: an M = 128, N = 64 MMA takes 48 cycles), and 8 us at each start of a unit.  256
+// sequences of 128K: 84 us and the merge, 4.7 TB/s of memory, every code read once, tensor pipe 24 % active.  Requesting
+// tiles into L2 ahead of the rings changed nothing at 1, 2 or 3 tiles.
 #pragma once
 
 #include "decode.cuh"
@@ -51,7 +56,7 @@ constexpr int kQdKept = 2048;              // units whose tile counts fit the P 
 // Cost of starting a unit, in tiles: query operand, refilled pipeline and record take about 8 us, a tile 4 us where all
 // SMs stream.  It lies before the unit's first tile, so a range that starts units holds fewer tiles.
 constexpr int kQdStart = 2;
-constexpr float kQdShift = 6.0f;           // the reference m lies this far (log2) below the maximum
+constexpr float kQdShift = 4.0f;           // the reference m lies this far (log2) below the maximum
 
 constexpr uint32_t kQsQ = 0;
 constexpr uint32_t kQsP = kQsQ + kDecQBytes;

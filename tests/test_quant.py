@@ -7,9 +7,9 @@ the bf16 window), and bf16 outputs add 2^-8 of themselves: |err| <= 2^-7 sum p|v
 2 delta sum p|v| where delta is how far a logit may be off (fp32 sums and exponentials, 2^-18 of
 sum |q||k| scale; with QK normalisation the query is rounded to 8 significant bits, 2^-8 of it).
 The 2^-7 holds where the e4m3 term is normal.  In the kernel's units (reference 2^-m, the row's largest
-p * 2^e, e the value's scale, held at 2^6 or more) that is p * 2^e >= 2^-6; below, the e4m3 term is off by at most
+p * 2^e, e the value's scale, held at 2^4 or more) that is p * 2^e >= 2^-6; below, the e4m3 term is off by at most
 half its last step, 2^-10, and the e5m2 term holds that to 2^-3 (or to 2^-17, half its last step): 2^-13 in all,
-which is 2^-13 / 2^6 = 2^-19 of max(p * 2^e) for
+which is 2^-13 / 2^4 = 2^-17 of max(p * 2^e) for
 each code of an entry that is multiplied with it."""
 import ctypes
 
@@ -351,7 +351,7 @@ def decode_case(dev, seed, lengths, Hq, Hkv, blk, W, ps=0, norm=False, gate=Fals
         s = torch.cat([torch.pow(2.0, vs[b, :nc[b]].double() - 127), torch.ones(nw, Hkv, dtype=torch.float64, device=dev)])
         lost = (p * s.T[:, None]).amax(-1)[..., None] * (vval[b, :nc[b]].abs() / s[:nc[b], :, None]).sum(0)[:, None]
         out[b] = o
-        tol[b] = 2.0 ** -19 * lost.reshape(Hq, 512) + mass * (2.0 ** -7 + 2 * d * (2.0 ** -8 if norm else 2.0 ** -18) + 2.0 ** -16)
+        tol[b] = 2.0 ** -17 * lost.reshape(Hq, 512) + mass * (2.0 ** -7 + 2 * d * (2.0 ** -8 if norm else 2.0 ** -18) + 2.0 ** -16)
     if gate:
         s = torch.sigmoid(gates.double())
         out, tol = out * s, tol * s
