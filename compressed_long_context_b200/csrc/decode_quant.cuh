@@ -15,6 +15,8 @@
 //       2^-7 off, 2^-10 in the mean square; below, hi is within 2^-10 and lo within 2^-3 of the rest: 2^-13, or
 //       2^-17 of the largest.  lo is e5m2 because its range matters more than its last bit: a probability down to
 //       2^-20 of the largest still has a term, so a long tail of small probabilities is kept.
+//   (bf16 keys: p as two bf16 terms, 2^-16, in the two P buffers: one term would be 2^-8 off, as much as the output's own
+//   rounding; short sequences, whose window weighs most, were 1.7 times further off with QK normalisation.)
 // The scale of a value vector belongs to the key, which is the contraction's axis, so it goes into p: with
 // y = z + log2(vscale), the accumulators hold sums of 2^(y - m) * code, the reference m is the running
 // maximum of y, and the row sum l adds 2^(y - m) / vscale = 2^(z - m).  m is kept 2^4 below the maximum
@@ -539,11 +541,13 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         const uint32_t id_w = idesc_bf16(128, kDecHeads, 1, 1);
         const uint32_t id_hi = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE4M3, 1, 1);
         const uint32_t id_lo = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE5M2, 1, 1);
-        uint32_t vs = 0;
-        for (int n = 0; !it.done; it.next(), ++n) {
-            const int b = n % kDecPBufs;
+        uint32_t vs = 0, pn = 0;                           // V slabs, P buffers used
+        for (; !it.done; it.next()) {
             const bool first = it.first(), codes = it.codes();
-            if (!warp_wait(&p_full[b], (n / kDecPBufs) & 1, abort_flag)) break;
+            const uint32_t b = pn % kDecPBufs, b2 = (pn + 1) % kDecPBufs;      // a bf16 tile's lo is in the second
+            if (!warp_wait(&p_full[b], (pn / kDecPBufs) & 1, abort_flag)) break;
+            if (!codes && !warp_wait(&p_full[b2], ((pn + 1) / kDecPBufs) & 1, abort_flag)) break;
+            pn += codes ? 1 : 2;
             if (first && !warp_wait(o_empty, (it.item & 1) ^ 1, abort_flag)) break;
             tc_fence_after();
             const int nvalid = it.nvalid();
@@ -578,6 +582,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 const uint32_t dst = tmem + kTmO + 64 * c;
                 const uint64_t vd = smem_desc_sw128(smem_u32(slab), kSlabBytes, 1024);
                 const uint64_t p8 = smem_desc_sw64(p_base, 8192, 512), pw = smem_desc_sw128(p_base, 8192, 1024);
+                const uint64_t pl = smem_desc_sw128(smem_u32(sm + kQsP + b2 * kDecPBytes), 8192, 1024);
                 if (elect_one()) {
                     if (E8 && codes) {
 #pragma unroll
@@ -590,8 +595,10 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)     // 16 keys each
-                            if (kk < steps)
+                            if (kk < steps) {
                                 mma_ss(dst, vd + kk * (2048 >> 4), pw + kk * (2048 >> 4), id_w, (first && kk == 0) ? 0u : 1u);
+                                mma_ss(dst, vd + kk * (2048 >> 4), pl + kk * (2048 >> 4), id_w, 1u);
+                            }
                         mma_commit(&empty_v[st]);
                         mma_commit(&empty_v[st + 1]);
                     }
@@ -601,6 +608,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             if (!ok) break;
             if (elect_one()) {
                 mma_commit(&p_empty[b]);
+                if (!codes) mma_commit(&p_empty[b2]);
                 if (it.last()) mma_commit(o_full);
             }
             __syncwarp();
@@ -631,7 +639,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
         // A wait of this warp ran out.  The warps leave together, at the barrier that every tile has; until then a
         // warp that gave up goes on without waiting for long (the abort flag is set).
         bool bad = false;
-        uint32_t nq = 0;
+        uint32_t nq = 0, pn = 0;              // query operands, P buffers used
         // A piece's record is written behind the making of the next piece's query operand, whose products then run
         // beside it.
         int rec = -1, rec_item = 0;
@@ -801,8 +809,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll
                     for (int h = 0; h < 32; ++h) lsum[h] *= al_s[h0 + h];
                     // rescale O^T once the previous PV has landed
-                    const int pb = (n - 1) % kDecPBufs;
-                    bad = !warp_wait(&p_empty[pb], ((n - 1) / kDecPBufs) & 1, abort_flag);
+                    bad = !warp_wait(&p_empty[(pn - 1) % kDecPBufs], ((pn - 1) / kDecPBufs) & 1, abort_flag);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -831,9 +838,10 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) lsum[h + e] = fmaf(z[h + e], rv, lsum[h + e]);
             }
-            const int pbuf = n % kDecPBufs;
-            if (!bad) bad = !warp_wait(&p_empty[pbuf], ((n / kDecPBufs) & 1) ^ 1, abort_flag);
-            uint8_t* pt = sm + kQsP + pbuf * kDecPBytes;
+            const uint32_t b = pn % kDecPBufs, b2 = (pn + 1) % kDecPBufs;
+            if (!bad) bad = !warp_wait(&p_empty[b], ((pn / kDecPBufs) & 1) ^ 1, abort_flag);
+            if (!bad && !codes) bad = !warp_wait(&p_empty[b2], (((pn + 1) / kDecPBufs) & 1) ^ 1, abort_flag);
+            uint8_t* pt = sm + kQsP + b * kDecPBytes;
             if (!bad) {
                 if (E8 && codes) {
 #pragma unroll
@@ -852,15 +860,27 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4*>(pt + sw128(r, 4 * hh + c)) =
-                            make_uint4(pack_bf16x2(z[8 * c], z[8 * c + 1]), pack_bf16x2(z[8 * c + 2], z[8 * c + 3]),
-                                       pack_bf16x2(z[8 * c + 4], z[8 * c + 5]), pack_bf16x2(z[8 * c + 6], z[8 * c + 7]));
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a0 = z[8 * c + 2 * e], a1 = z[8 * c + 2 * e + 1];
+                            hi[e] = pack_bf16x2(a0, a1);
+                            lo[e] = pack_bf16x2(a0 - bf16lo(hi[e]), a1 - bf16hi(hi[e]));
+                        }
+                        *reinterpret_cast<uint4*>(pt + sw128(r, 4 * hh + c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(sm + kQsP + b2 * kDecPBytes + sw128(r, 4 * hh + c)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[pbuf]);
+                if (lane == 0) {
+                    mbar_arrive(&p_full[b]);
+                    if (!codes) mbar_arrive(&p_full[b2]);
+                }
             }
+            pn += codes ? 1 : 2;
 
             if (last) {
                 // ---- end of this CTA's piece of unit u: the row sums over all key rows for its record
