@@ -21,7 +21,7 @@
 // y = z + log2(vscale), the accumulators hold sums of 2^(y - m) * code, the reference m is the running
 // maximum of y, and the row sum l adds 2^(y - m) / vscale = 2^(z - m).  m is kept 2^4 below the maximum
 // and moves when some y exceeds it by 2^8, so that p <= 256 and 2^4 for the largest key: e4m3 ends at 448.  (2^6
-// moved it, and with it 64 KB of accumulators, in most tiles of the ragged batch: 166 us, 2^4: 159.)
+// moved it, and with it 128 KB of accumulators, in most tiles of the ragged batch: 4 % of its time.)
 // The same kernel with bf16 entries (E8 = false) attends what the sequences of hca_decode_shared do not have in
 // common: then all tiles are of the window's kind, and the reference moves at 2^32 (bf16 holds any p).
 //
@@ -759,10 +759,8 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             const uint32_t sc_next = last ? 0u : scales(it.tile + 1);      // loaded while this tile is worked on
             if (!bad) bad = !warp_wait(&s_full[sb], (n / look) & 1, abort_flag);
             tc_fence_after();
-            float z[32];
-            tmem_ld32(tmem + lane_off + dec_s_col(sb) + h0, z);
             float kscale = q_scale(sc & 0xffu);
-            if (NORM) {
+            if (NORM) {                      // (ahead of the logits: both at once would not fit the registers)
                 float d[32];
                 tmem_ld32(tmem + lane_off + kTmKK + q4 * 32, d);
                 tmem_wait_ld32(d);
@@ -771,6 +769,8 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 for (int j = 0; j < 32; ++j) diag = (j == lane) ? d[j] : diag;
                 kscale *= rsqrtf(diag * (1.f / kDecD) * kscale * kscale + p.eps);
             }
+            float z[32];
+            tmem_ld32(tmem + lane_off + dec_s_col(sb) + h0, z);
             tmem_wait_ld32(z);
             tc_fence_before();
             __syncwarp();
