@@ -412,7 +412,8 @@ hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales,
  * hca_decode_vha (Hkv == 1), else NULL; gq, gk 16-byte aligned; every other argument, the workspace (hca_decode_workspace_size)
  * and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row: its output is zero.
  * Arithmetic: codes go to the tensor cores as they are; the query and the probabilities are split into
- * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.
+ * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.  Value scales of one sequence that
+ * lie more than 2^60 apart may cost the keys of the smaller ones their weight.
  */
 hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, const void* scales,
                               const int* page_table, int page_size, int max_pages, int num_pages,
@@ -431,7 +432,8 @@ hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, con
  * inside the prefix sees only the part before its window.  Np == 0 is a batch without a prefix (kp, vp NULL).
  * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v, gq, gk as for hca_decode_quant;
  * every other argument and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row:
- * its output is zero.  The workspace: hca_decode_shared_workspace_size bytes.
+ * its output is zero.  The prefix's entries are finite: one that is not may reach sequences that do not see it.
+ * The workspace: hca_decode_shared_workspace_size bytes.
  */
 size_t hca_decode_shared_workspace_size(int B, int Hq, int Hkv, int dv, int Np);
 hca_status_t hca_decode_shared(const void* q, const void* kp, const void* vp, const void* kc, const void* vc,
