@@ -1042,32 +1042,39 @@ bool cache_geometry(bool paged, const int* page_table, int page_size, int max_pa
     return Nmax >= 1;
 }
 
-// The merge pass after the passes that wrote the records; it may start while they still run.
-hca_status_t launch_merge(const hca::MergeParams& mp, bool prefix, cudaStream_t s) {
+template <int kChunk, int CH>
+hca_status_t launch_merge_as(const hca::MergeParams& mp, bool prefix, cudaStream_t s) {
     using namespace hca;
-    const long long U = (long long)mp.B * mp.Hkv;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)U, (unsigned)(kDecD / kMergeCh));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = mp.vha_u ? combine_vha_smem(mp.vha_r) : 0;
+    cfg.gridDim = dim3((unsigned)(mp.B * mp.Hkv), (unsigned)(kDecD / CH));
+    cfg.blockDim = dim3(MergeShape<CH>::kThreads);
+    cfg.dynamicSmemBytes = mp.vha_u ? merge_vha_smem<CH>(mp.vha_r) : 0;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // records loaded per round, from the average number of pieces per unit (about nsplit / U)
-    const bool wide = (long long)mp.nsplit >= 3 * U;
     using Fn = void (*)(const MergeParams);
-    const Fn fns[2][2][2] = {{{merge_kernel<2, false, false>, merge_kernel<2, false, true>},
-                              {merge_kernel<2, true, false>, merge_kernel<2, true, true>}},
-                             {{merge_kernel<4, false, false>, merge_kernel<4, false, true>},
-                              {merge_kernel<4, true, false>, merge_kernel<4, true, true>}}};
-    if (cudaLaunchKernelEx(&cfg, fns[wide][mp.vha_u != nullptr][prefix], mp) != cudaSuccess) {
+    const Fn fns[2][2] = {{merge_kernel<kChunk, CH, false, false>, merge_kernel<kChunk, CH, false, true>},
+                          {merge_kernel<kChunk, CH, true, false>, merge_kernel<kChunk, CH, true, true>}};
+    if (cudaLaunchKernelEx(&cfg, fns[mp.vha_u != nullptr][prefix], mp) != cudaSuccess) {
         cudaGetLastError();
         return HCA_ERR_CUDA;
     }
     return HCA_OK;
+}
+
+// The merge pass after the passes that wrote the records; it may start while they still run.  Records per round go by the
+// average number of pieces per unit, nsplit / U: many pieces, eight (one sequence of 1M tokens, 65 pieces: 25.6
+// against 32.0 us with four and fewer CTAs) or four (16 of
+// 512K: 35.1 against 35.8 us with two), few, two (64 of 128K: 38.5 against 39.5 us with four).  Few units also take
+// channels eight at a time, for more CTAs than SMs.
+hca_status_t launch_merge(const hca::MergeParams& mp, bool prefix, cudaStream_t s) {
+    const long long U = (long long)mp.B * mp.Hkv;
+    if (16 * U <= mp.nsplit) return launch_merge_as<8, 8>(mp, prefix, s);
+    if (3 * U <= mp.nsplit) return launch_merge_as<4, 32>(mp, prefix, s);
+    return launch_merge_as<2, 32>(mp, prefix, s);
 }
 
 }  // namespace

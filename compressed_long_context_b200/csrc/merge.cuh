@@ -6,10 +6,10 @@
 // 2^(z - m) and the 512 sums of 2^(z - m) v.  hca_decode_shared adds a second kind: the shared prefix
 // of 2 * (128 / G) sequences at once.
 //
-// Grid (units, 512 / 32), 256 threads: a CTA owns all G heads of one unit for 32 channels, so the mixing across
-// heads stays on chip.  Thread = (4 channels, heads hb, hb + 32): a warp reads whole 128-byte
-// lines of four heads.  The records of a chunk are all loaded before any is used (one memory round trip for up to
-// kChunk of them).
+// Grid (units, 512 / CH): a CTA owns all G heads of one unit for CH channels, so the mixing across heads stays on chip.
+// Thread = (4 channels, kHeads heads): a warp reads whole 128-byte lines of four heads (CH = 32) or 32-byte sectors of 16
+// (CH = 8).  The records of a chunk are all loaded before any is used (one memory round trip for up to kChunk of
+// them).  What bounds it: the records, which lie in L2, and two dependent round trips.
 #pragma once
 
 #include "decode.cuh"
@@ -79,23 +79,32 @@ struct MergeParams {
     const SharedPlan* plan;
 };
 
-constexpr int kMergeHeads = 2;            // heads per thread
-constexpr int kMergeThreads = 256;
-constexpr int kMergeStep = kMergeThreads / 8;    // a thread's heads are this far apart
+template <int CH>
+struct MergeShape {
+    static constexpr int kThreads = CH == 32 ? 256 : 128;
+    static constexpr int kStep = kThreads / (CH / 4);         // a thread's heads are this far apart
+    static constexpr int kHeads = kDecHeads / kStep;          // heads per thread
+};
+template <int CH>
+constexpr uint32_t merge_vha_smem(int r) {
+    return (uint32_t)(2 * kDecHeads * r + kDecHeads * CH + r * CH) * 4u;
+}
 
-template <int kChunk, bool kVha, bool kPfx>
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
+template <int kChunk, int CH, bool kVha, bool kPfx>
+__global__ void __launch_bounds__(MergeShape<CH>::kThreads) merge_kernel(const MergeParams p) {
+    constexpr int kMergeThreads = MergeShape<CH>::kThreads, kMergeStep = MergeShape<CH>::kStep, kMergeHeads = MergeShape<CH>::kHeads;
+    constexpr int kLanes = CH / 4;                    // threads of one head
     extern __shared__ float cs[];
     const int u = blockIdx.x;
-    const int hb = threadIdx.x >> 3;
-    const int c4 = 4 * (threadIdx.x & 7);
-    const int c = blockIdx.y * kMergeCh + c4;                       // channels c .. c+3
+    const int hb = threadIdx.x / kLanes;
+    const int c4 = 4 * (threadIdx.x % kLanes);
+    const int c = blockIdx.y * CH + c4;                       // channels c .. c+3
     const int b = p.Hkv == 1 ? u : u / p.Hkv, g = u - b * p.Hkv;
     const size_t orow = ((size_t)b * p.Hq + (size_t)g * p.G + hb) * kDecD + c;
     const int R = p.vha_r;
-    float* os = cs;                                   // [64][32] merged, gated outputs (16-byte rows)
-    float* ts = os + kDecHeads * kMergeCh;            // [R][32]  V^T o
-    float* vs = ts + R * kMergeCh;                    // [G][R]
+    float* os = cs;                                   // [64][CH] merged, gated outputs (16-byte rows)
+    float* ts = os + kDecHeads * CH;                  // [R][CH]  V^T o
+    float* vs = ts + R * CH;                          // [G][R]
     float* us = vs + kDecHeads * R;                   // [G][R]
     // the inputs are not products of the passes before: read while those still run
     uint2 graw[kMergeHeads];
@@ -202,25 +211,25 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
         // o'[:, ch] = o[:, ch] + U (V^T o[:, ch]) over the G heads of this token (see decode.cuh)
 #pragma unroll
         for (int x = 0; x < kMergeHeads; ++x)
-            if (hb + kMergeStep * x < p.G) *reinterpret_cast<float4*>(os + (hb + kMergeStep * x) * kMergeCh + c4) = r[x];
+            if (hb + kMergeStep * x < p.G) *reinterpret_cast<float4*>(os + (hb + kMergeStep * x) * CH + c4) = r[x];
         __syncthreads();
-        for (int i = threadIdx.x; i < R * (kMergeCh / 4); i += kMergeThreads) {
-            const int k = i >> 3, cc = (i & 7) * 4;
+        for (int i = threadIdx.x; i < R * kLanes; i += kMergeThreads) {
+            const int k = i / kLanes, cc = (i % kLanes) * 4;
             float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int hd = 0; hd < p.G; ++hd) {
                 const float vk = vs[hd * R + k];
-                const float4 o4 = *reinterpret_cast<const float4*>(os + hd * kMergeCh + cc);
+                const float4 o4 = *reinterpret_cast<const float4*>(os + hd * CH + cc);
                 t.x = fmaf(vk, o4.x, t.x);
                 t.y = fmaf(vk, o4.y, t.y);
                 t.z = fmaf(vk, o4.z, t.z);
                 t.w = fmaf(vk, o4.w, t.w);
             }
-            *reinterpret_cast<float4*>(ts + k * kMergeCh + cc) = t;
+            *reinterpret_cast<float4*>(ts + k * CH + cc) = t;
         }
         __syncthreads();
         for (int k = 0; k < R; ++k) {
-            const float4 t4 = *reinterpret_cast<const float4*>(ts + k * kMergeCh + c4);
+            const float4 t4 = *reinterpret_cast<const float4*>(ts + k * CH + c4);
 #pragma unroll
             for (int x = 0; x < kMergeHeads; ++x) {
                 if (hb + kMergeStep * x >= p.G) continue;
