@@ -89,8 +89,9 @@ __device__ __forceinline__ void pool_rows_quant(const __nv_bfloat16* __restrict_
 #pragma unroll
         for (int u = 0; u < kPoolUnroll; ++u) {
             const int rr = r + u * R;
-            if (rr < blk) {
-                const float a = alpha[rr];
+            // a token without weight (w = -inf: padding) may hold anything
+            const float a = rr < blk ? alpha[rr] : 0.f;
+            if (a != 0.f) {
                 acc[0] = fmaf(a, bf16lo(x[u].x), acc[0]);
                 acc[1] = fmaf(a, bf16hi(x[u].x), acc[1]);
                 acc[2] = fmaf(a, bf16lo(x[u].y), acc[2]);
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_quant_kernel(const Appe
     const float s_new = fmaf(s_old, a, e);
     const bool complete = (pos + 1) % p.blk == 0;
     auto fold = [&](uint2 x, float4& t) {
+        if (e == 0.f) x = make_uint2(0u, 0u);       // a token without weight may hold anything
         t.x = fmaf(e, bf16lo(x.x), t.x * a);
         t.y = fmaf(e, bf16hi(x.x), t.y * a);
         t.z = fmaf(e, bf16lo(x.y), t.z * a);

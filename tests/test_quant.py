@@ -601,3 +601,31 @@ def test_decode_not_finite_query(cuda_device, libhca):
     rest = [h for h in range(64) if h not in (5, 9)]
     assert torch.isnan(got[0, 5]).all() and torch.isnan(got[0, 9]).all()
     check(got[:, rest], out[:, rest], tol[:, rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, 1])
+def test_tokens_without_weight(cuda_device, libhca, first):
+    """Tokens of weight -inf may hold NaN or infinities: the entry is that of the others, written at once or token by token."""
+    dev, g = cuda_device, torch.Generator(device=cuda_device).manual_seed(4)
+    blk, d = 8, 64
+    k, v = (torch.randn(1, blk, 1, d, generator=g, device=dev).to(bf) for _ in range(2))
+    w = torch.randn(1, blk, generator=g, device=dev)
+    none = [first, 5]
+    w[0, none] = float("-inf")
+    clean = [hca.compress_quant(*(torch.where((w == float("-inf"))[..., None, None], 0, x) for x in (k, v)), w, blk=blk)]
+    for x in (k, v):
+        x[0, none[0]], x[0, none[1]] = float("nan"), float("inf")
+    clean.append(hca.compress_quant(k, v, w, blk=blk))
+    kw = torch.zeros(1, 4, 1, d, dtype=bf, device=dev)
+    kc, vc, sc = (torch.zeros_like(x.view(torch.uint8)).view(x.dtype) for x in clean[0])
+    st = torch.zeros(hca.append_state_size(1, 1, d, d), dtype=torch.uint8, device=dev)
+    for t in range(blk):
+        hca.append_quant(k[:, t].contiguous(), v[:, t].contiguous(), w[:, t].contiguous(),
+                         torch.tensor([t + 1], dtype=torch.int32, device=dev), kw, kw.clone(), kc, vc, sc, st, blk)
+    done()
+    val = lambda c, s, i: c.float() * s.float()[..., i:i + 1]  # noqa: E731
+    for i in range(2):
+        a, b, c = (val(x[i], x[2], i) for x in (clean[0], clean[1], (kc, vc, sc)))
+        step = torch.maximum(2.0 ** -3 * a.abs(), 2.0 ** -9 * clean[0][2].float()[..., i:i + 1])
+        assert torch.equal(a, b) and bool(((c - a).abs() <= step).all())
