@@ -6,7 +6,7 @@
 // is raw bf16.  Entries go from memory to the tensor cores as they are (kind::f8f6f4, K = 32): widening
 // them on the way would cost more shared-memory bandwidth than HBM delivers bytes (write 64 KB, read 64 KB,
 // write 128 KB, read 128 KB per 128 keys of K and again of V).  The other operands are bf16 quantities, so
-// each is split into two 8-bit terms, both multiplied with the same 8-bit tile into one fp32 accumulator:
+// each is split into two 8-bit terms, both multiplied with the same 8-bit tile in fp32:
 //   q = hi + lo, both e4m3, after a power-of-two scale per head that puts max|q| in (224, 448].  hi keeps 4
 //       significant bits and lo the next 4: a bf16 query (8 bits) is represented exactly down to 2^-10 of its
 //       head's largest channel, and to 2^-18.8 of that channel below.  Same rounding (2^-8 at most) as bf16
@@ -52,18 +52,21 @@ namespace hca {
 constexpr int kQdThreads = 384;
 constexpr int kQdSoftWarp0 = 4;
 constexpr int kQdRing = 4;                 // slabs per ring (K, V)
-constexpr int kQdLook = 4;                 // S buffers (2 with QK normalisation)
-constexpr int kQdLookNorm = 2;
+constexpr int kQdLook = 4;                 // S buffers at most
+// Tensor memory: S buffers (and K K^T) in columns 0 .. 255, O^T in 256 .. 511 (4 x 64 for 128 channels each).
+constexpr uint32_t kQdKK = 128, kQdO = 256;
 constexpr int kQdKept = 2048;              // units whose tile counts fit the P buffers while these are not in use
 // Cost of starting a unit, in tiles: query operand, refilled pipeline and record take about 8 us, a tile 4 us where all
 // SMs stream.  It lies before the unit's first tile, so a range that starts units holds fewer tiles.
 constexpr int kQdStart = 2;
 constexpr float kQdShift = 4.0f;           // the reference m lies this far (log2) below the maximum
 
+// Shared memory: query operand (8 tiles of 8 KB: 64 bf16 channels of each head, or 128 codes) and K ring, 64 KB each; P
+// buffers; V ring.
+constexpr uint32_t kQdQTile = 8192;
 constexpr uint32_t kQsQ = 0;
-constexpr uint32_t kQsP = kQsQ + kDecQBytes;
-constexpr uint32_t kQsK = kQsP + kDecPBufs * kDecPBytes;
-constexpr uint32_t kQsV = kQsK + kQdRing * kSlabBytes;
+constexpr uint32_t kQsP = kDecQBytes + kQdRing * kSlabBytes;
+constexpr uint32_t kQsV = kQsP + kDecPBufs * kDecPBytes;
 constexpr uint32_t kQsBar = kQsV + kQdRing * kSlabBytes;
 constexpr int kQdBars = 4 * kQdRing + 3 + 2 * kQdLook + 2 * kDecPBufs + 2;
 constexpr uint32_t kQsRed = (kQsBar + kQdBars * 8 + 127) & ~127u;   // float[4][64]
@@ -74,7 +77,28 @@ constexpr uint32_t kQsMisc = kQsQscale + 64 * 4;
 constexpr uint32_t kQdSmem = kQsMisc + 128;
 static_assert(kQdKept * 8 <= kDecPBufs * kDecPBytes, "kept tile counts fit the P buffers");
 static_assert(kQdSmem <= 232448, "decode_quant shared memory exceeds the 227 KB per-block limit");
-static_assert(kQsRed % 16 == 0 && kQsK % 1024 == 0 && kQsV % 1024 == 0, "alignment");
+static_assert(kQsRed % 16 == 0 && kQsP % 1024 == 0 && kQsV % 1024 == 0, "alignment");
+
+// Codes with QK normalisation ("joined"): two tiles of the query operand and a slot of the K ring alternate, so that slab s of
+// a tile of codes, which always lies in slot s, continues q hi and q lo of its channels: one MMA of N = 256 multiplies the slab
+// with hi, lo and itself, into one buffer of [hi 64 | lo 64 | K K^T 128] columns.  It takes 128 cycles, where three MMAs take
+// 48 + 48 + 64 (128 ragged sequences 164.7 -> 161.1 us).  Else the operand lies in front of the ring, hi and lo go into one
+// accumulator, and the S buffers have 64 columns: the alternating layout was slower there, with one MMA of N = 128 or two of
+// N = 64 (64 sequences of 128K 40.0 against 39.4 us).
+template <bool NORM, bool E8>
+struct QdShape {
+    static constexpr bool kJoined = NORM && E8;
+    static constexpr int kLook = kJoined ? 1 : (NORM ? 2 : 4);                                // S buffers
+    static constexpr uint32_t kK = kJoined ? 2 * kQdQTile : kDecQBytes;                       // K slot s at kK + s * kSlot
+    static constexpr uint32_t kSlot = kJoined ? 2 * kQdQTile + kSlabBytes : kSlabBytes;
+    static constexpr uint32_t kHi = kJoined ? kSlot : kQdQTile;                               // q hi of slab s at s * kHi
+    static constexpr uint32_t kLo = kJoined ? kQdQTile : 4 * kQdQTile;                        // q lo behind q hi
+    // tile s of the bf16 operand
+    __host__ __device__ static constexpr uint32_t q_tile(uint32_t s) {
+        return kJoined ? (s >> 1) * kSlot + (s & 1) * kQdQTile : s * kQdQTile;
+    }
+};
+static_assert(2 * kQdQTile == kSlabBytes && 8 * kQdQTile == kDecQBytes, "operand tiles and slots share one aligned grid");
 
 struct QuantParams {
     const int* seqlens;            // [B]
@@ -413,7 +437,9 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    constexpr int look = NORM ? kQdLookNorm : kQdLook;
+    using Shape = QdShape<NORM, E8>;
+    constexpr int look = Shape::kLook;
+    constexpr bool joined = Shape::kJoined;
     QIter<E8> it;
     it.init(&p, *range);
 
@@ -423,7 +449,8 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             const bool is_v = warp == 3;
             uint64_t* full = is_v ? full_v : full_k;
             uint64_t* empty = is_v ? empty_v : empty_k;
-            uint8_t* ring = sm + (is_v ? kQsV : kQsK);
+            uint8_t* ring = sm + (is_v ? kQsV : Shape::kK);
+            const uint32_t slot = is_v ? kSlabBytes : Shape::kSlot;
             const CUtensorMap* mc = is_v ? &tm_v : &tm_k;
             const CUtensorMap* mw = is_v ? &tm_vw : &tm_kw;
             // test switch (hca_debug_set_drop_slab): the first K slab is never requested
@@ -448,7 +475,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                         ok = false;                                                  // consumer's wait runs out
                         break;
                     }
-                    uint8_t* dst = ring + st * kSlabBytes;
+                    uint8_t* dst = ring + st * slot;
                     mbar_arrive_expect_tx(&full[st], halves && !h1 ? kSlabBytes / 2 : kSlabBytes);
                     if (halves) {
                         tma_load_4d(dst, mc, &full[st], wide * s, it.t.g, j0 % p.page_size, pg[0]);
@@ -464,8 +491,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
     } else if (warp == 1) {
         // ===================================================== QK^T issuer (warp waits, one lane issues)
         const uint32_t id_w = idesc_bf16(128, kDecHeads, 0, 0), id_wkk = idesc_bf16(128, 128, 0, 0);
-        const uint32_t id_e = idesc_f8(128, kDecHeads, kFmtE4M3, kFmtE4M3, 0, 0);
-        const uint32_t id_ekk = idesc_f8(128, 128, kFmtE4M3, kFmtE4M3, 0, 0);
+        const uint32_t id_e = idesc_f8(128, joined ? 256 : kDecHeads, kFmtE4M3, kFmtE4M3, 0, 0);
         const uint32_t q_base = smem_u32(sm + kQsQ);
         uint32_t ks = 0, nq = 0, nconv = 0;
         for (int n = 0; !it.done; it.next(), ++n) {
@@ -479,7 +505,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     mbar_arrive_expect_tx(q_tma, kDecQBytes);
 #pragma unroll 1
                     for (int s = 0; s < kDecSlabs; ++s)
-                        tma_load_4d(sm + kQsQ + s * 8192, &tm_q, q_tma, 64 * s, it.t.g * p.G, it.t.b, 0);
+                        tma_load_4d(sm + kQsQ + Shape::q_tile(s), &tm_q, q_tma, 64 * s, it.t.g * p.G, it.t.b, 0);
                 }
                 __syncwarp();
                 ++nq;
@@ -494,7 +520,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             // the K K^T accumulator has one buffer: wait until tile n-1's softmax has read it
             if (NORM && n > 0 && !warp_wait(&s_empty[(n - 1) % look], ((n - 1) / look) & 1, abort_flag)) break;
             tc_fence_after();
-            const uint32_t dst = tmem + dec_s_col(sb);
+            const uint32_t dst = tmem + 64 * sb;
             const int ns = codes ? 4 : 8;
             bool ok = true;
 #pragma unroll 1
@@ -505,22 +531,22 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     break;
                 }
                 tc_fence_after();
-                const uint64_t kd = smem_desc_sw128(smem_u32(sm + kQsK + st * kSlabBytes), 16, 1024);
-                const uint64_t qd = smem_desc_sw128(q_base + s * 8192, 16, 1024);
+                const uint64_t kd = smem_desc_sw128(smem_u32(sm + Shape::kK + st * Shape::kSlot), 16, 1024);
+                const uint32_t q_off = codes ? s * Shape::kHi : Shape::q_tile(s);
+                const uint64_t qd = smem_desc_sw128(q_base + q_off, 16, 1024);
                 if (elect_one()) {
                     // descriptors advance by 32 bytes (2 of their units) per step
                     if (E8 && codes) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             mma_f8(dst, kd + 2 * kk, qd + 2 * kk, id_e, (s | kk) ? 1u : 0u);
-                            mma_f8(dst, kd + 2 * kk, qd + (32768 >> 4) + 2 * kk, id_e, 1u);
-                            if (NORM) mma_f8(tmem + kTmKK, kd + 2 * kk, kd + 2 * kk, id_ekk, (s | kk) ? 1u : 0u);
+                            if (!joined) mma_f8(dst, kd + 2 * kk, qd + (Shape::kLo >> 4) + 2 * kk, id_e, 1u);
                         }
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             mma_ss(dst, kd + 2 * kk, qd + 2 * kk, id_w, (s | kk) ? 1u : 0u);
-                            if (NORM) mma_ss(tmem + kTmKK, kd + 2 * kk, kd + 2 * kk, id_wkk, (s | kk) ? 1u : 0u);
+                            if (NORM) mma_ss(tmem + kQdKK, kd + 2 * kk, kd + 2 * kk, id_wkk, (s | kk) ? 1u : 0u);
                         }
                     }
                     mma_commit(&empty_k[st]);
@@ -579,7 +605,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                     __syncwarp();
                 }
                 tc_fence_after();
-                const uint32_t dst = tmem + kTmO + 64 * c;
+                const uint32_t dst = tmem + kQdO + 64 * c;
                 const uint64_t vd = smem_desc_sw128(smem_u32(slab), kSlabBytes, 1024);
                 const uint64_t p8 = smem_desc_sw64(p_base, 8192, 512), pw = smem_desc_sw128(p_base, 8192, 1024);
                 const uint64_t pl = smem_desc_sw128(smem_u32(sm + kQsP + b2 * kDecPBytes), 8192, 1024);
@@ -668,8 +694,9 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll 2
                     for (int i = 0; i < 8; ++i) {
                         const int h = warp - kQdSoftWarp0 + kDecSoftWarps * i;
-                        uint4* src0 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3)));
-                        uint4* src1 = reinterpret_cast<uint4*>(sm + kQsQ + (lane >> 2) * 8192 + sw128(h, 2 * (lane & 3) + 1));
+                        uint8_t* row = sm + kQsQ + Shape::q_tile(lane >> 2);
+                        uint4* src0 = reinterpret_cast<uint4*>(row + sw128(h, 2 * (lane & 3)));
+                        uint4* src1 = reinterpret_cast<uint4*>(row + sw128(h, 2 * (lane & 3) + 1));
                         const uint4 xa = *src0, xb = *src1;
                         const uint32_t w8[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
                         float f[16];
@@ -714,9 +741,9 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                                 lo[e] = l0 | l1 << 16;
                             }
                             __syncwarp();                    // every lane has read its part of the row
-                            uint8_t* dst = sm + kQsQ + (lane >> 3) * 8192 + sw128(h, lane & 7);
+                            uint8_t* dst = sm + kQsQ + (lane >> 3) * Shape::kHi + sw128(h, lane & 7);
                             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + 32768) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(dst + Shape::kLo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                             if (lane == 0) qs_s[h] = q_scale(byte) * p.scale_log2;
                         } else {
                             *src0 = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -742,7 +769,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     float o[32];
-                    tmem_ld32(tmem + lane_off + kTmO + 64 * c + h0, o);
+                    tmem_ld32(tmem + lane_off + kQdO + 64 * c + h0, o);
                     tmem_wait_ld32(o);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -762,7 +789,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
             float kscale = q_scale(sc & 0xffu);
             if (NORM) {                      // (ahead of the logits: both at once would not fit the registers)
                 float d[32];
-                tmem_ld32(tmem + lane_off + kTmKK + q4 * 32, d);
+                tmem_ld32(tmem + lane_off + kQdKK + q4 * 32, d);
                 tmem_wait_ld32(d);
                 float diag = 0.f;
 #pragma unroll
@@ -770,8 +797,18 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 kscale *= rsqrtf(diag * (1.f / kDecD) * kscale * kscale + p.eps);
             }
             float z[32];
-            tmem_ld32(tmem + lane_off + dec_s_col(sb) + h0, z);
+            tmem_ld32(tmem + lane_off + 64 * sb + h0, z);
             tmem_wait_ld32(z);
+            if (joined && codes) {           // the share of q lo
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float zl[16];
+                    tmem_ld16(tmem + lane_off + 64 * sb + 64 + h0 + 16 * c, zl);
+                    tmem_wait_ld16(zl);
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) z[16 * c + h] += zl[h];
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[sb]);
@@ -814,7 +851,7 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
-                        const uint32_t ta = tmem + lane_off + kTmO + 64 * c + h0;
+                        const uint32_t ta = tmem + lane_off + kQdO + 64 * c + h0;
                         tmem_ld32(ta, o);
                         tmem_wait_ld32(o);
                         uint32_t w[32];
