@@ -88,22 +88,29 @@ __device__ __forceinline__ void pool_rows_quant(const __nv_bfloat16* __restrict_
             if (tid < 32) block_alpha(w, pos0, blk, alpha);
             __syncthreads();
         }
+        // a pass's own sums: shorter chains of roundings (codes that differ from 64-bit pooling's, of 21 million: 99 instead of
+        // 130; torch's fp32 sums 121), for 0.5 of 45 us
+        float part[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[i] = 0.f;
 #pragma unroll
         for (int u = 0; u < kPoolUnroll; ++u) {
             const int rr = r + u * R;
             // a token without weight (w = -inf: padding) may hold anything
             const float a = rr < blk ? alpha[rr] : 0.f;
             if (a != 0.f) {
-                acc[0] = fmaf(a, bf16lo(x[u].x), acc[0]);
-                acc[1] = fmaf(a, bf16hi(x[u].x), acc[1]);
-                acc[2] = fmaf(a, bf16lo(x[u].y), acc[2]);
-                acc[3] = fmaf(a, bf16hi(x[u].y), acc[3]);
-                acc[4] = fmaf(a, bf16lo(x[u].z), acc[4]);
-                acc[5] = fmaf(a, bf16hi(x[u].z), acc[5]);
-                acc[6] = fmaf(a, bf16lo(x[u].w), acc[6]);
-                acc[7] = fmaf(a, bf16hi(x[u].w), acc[7]);
+                part[0] = fmaf(a, bf16lo(x[u].x), part[0]);
+                part[1] = fmaf(a, bf16hi(x[u].x), part[1]);
+                part[2] = fmaf(a, bf16lo(x[u].y), part[2]);
+                part[3] = fmaf(a, bf16hi(x[u].y), part[3]);
+                part[4] = fmaf(a, bf16lo(x[u].z), part[4]);
+                part[5] = fmaf(a, bf16hi(x[u].z), part[5]);
+                part[6] = fmaf(a, bf16lo(x[u].w), part[6]);
+                part[7] = fmaf(a, bf16hi(x[u].w), part[7]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += part[i];
     }
     // rows of one warp first (narrow rows: several to a warp), then across warps
     constexpr int RW = TPR < 32 ? 32 / TPR : 1;
