@@ -325,6 +325,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 2^x with the hardware approximation (PTX ex2.approx.ftz.f32: relative error about 2^-22,
 // results below 2^-126 flushed to zero, 2^-inf = 0).  The library exp2f adds range handling
 // that doubles the cost of a softmax; nothing here needs denormal results.

@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kPrepThreads) prefix_prep_kernel(const PrefixP
 
 // A row's reference moves when a logit exceeds it by this (log2).  P = 2^(z - m) is a floating number, so its
 // relative precision does not depend on m; the bound only keeps sums of P v in range (|v| < 2^80), and is wide
-// because a move costs a second pass over the unit and a rescaling of O (9000 cycles at most, against 6200 for
-// a tile's products): with 2^8 and one key in a hundred 8 times larger, every second unit of 8191 entries moved.
+// because a move costs a rescaling of O (thousands of cycles, against 6200 for a tile): with 2^8 and one key in a
+// hundred 8 times larger, every second unit of 8191 entries moved.
 constexpr float kPxRescale = 32.f;
 constexpr int kPxRing = 6;                        // 16 KB slabs of K, or units of V, in flight per SM
 constexpr uint32_t kPxSlab = 16384;               // K: 128 keys x 64 channels; V: 64 keys x 128 channels
@@ -184,7 +184,8 @@ enum : int {
     kPxPCons = 16,                                // P unit consumed: all four
     kPxPFull = 20, kPxCorr = 24,                  // P unit landed (each O rank) / checked and rescaled (leader)
     kPxOFull = 28, kPxOEmpty = 29, kPxDrain = 30,
-    kPxQFull = 32, kPxQEmpty = 40                 // per Q slab: landed (leader) / free (both)
+    kPxQFull = 32, kPxQEmpty = 40,                // per Q slab: landed (leader) / free (both)
+    kPxXch = 48                                   // maxima of an S tile exchanged, per TMEM lane quarter
 };
 
 __device__ __forceinline__ uint32_t px_idesc(int N, int b_mn) { return idesc_bf16(256, N, 0, b_mn); }
@@ -268,6 +269,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             mbar_init(&bars[kPxPFull + i], 4);         // armed by each TMEM lane quarter
             mbar_init(&bars[kPxCorr + i], 8);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[kPxXch + i], 2);
         mbar_init(&bars[kPxOFull], 1);
         mbar_init(&bars[kPxOEmpty], 16);
         mbar_init(&bars[kPxDrain], 1);
@@ -400,34 +402,53 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
         // ===================================================== S pair: softmax, P to the O pair
         // Eight warps: warp w owns the 32 rows of TMEM lane quarter w % 4 and one half of the
         // columns of every unit (hw = 0: the first 64, hw = 1: the last 64).  The two warps of
-        // a quarter keep identical per-row references m (they take the same decisions from
-        // the same exchanged maxima).
+        // a quarter keep identical per-row references m (they take the same decisions from the same
+        // exchanged maxima), and take them for a whole tile before its first store: stores of
+        // st.async to one address land in no order, so a unit is not stored again.
         if (go) {
             const int q4 = warp & 3;
             const int hw = (warp - 2) >> 2;
             const int r = q4 * 32 + lane;
             const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+            const bool neg = p.scale_log2 < 0.f;                      // of a row's logits, the least is then the largest
+            const int c0 = 64 * hw;                                   // this warp's columns of a unit
             float* xch = reinterpret_cast<float*>(sm + kPpSmXch);     // [2 parities][2 halves][128 rows]
-            int xpar = 0;
-            // a value of this row from both warps of the quarter (64-thread named barrier)
-            auto exchange = [&](float mine, float* other) {
-                xch[(xpar * 2 + hw) * 128 + r] = mine;
-                asm volatile("bar.sync %0, 64;" :: "r"(4 + q4) : "memory");
-                *other = xch[(xpar * 2 + (hw ^ 1)) * 128 + r];
-                xpar ^= 1;
-            };
-            // a condition of either warp of a quarter, which go on or unwind together: a verdict that differed
-            // would leave one of them at a named barrier the other never reaches
-            auto pair_any = [&](bool mine) -> bool {
-                uint32_t res;
-                asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                             "barrier.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                             : "=r"(res) : "r"((uint32_t)mine), "r"(4 + q4) : "memory");
-                return res != 0;
-            };
-            const uint32_t rP = peer_base + kPpSmP + (uint32_t)r * 16u;
+            const uint32_t rP = peer_base + kPpSmP + (uint32_t)r * 16u + (uint32_t)hw * 16384u;
             const uint32_t rHdr = peer_base + kPpSmHdr;
             const uint32_t rPFull = peer_base + kPpSmBar + kPxPFull * 8;
+            // S tile n, of whose columns this row sees the first `hi`: wait for it, and give the other warp of the quarter the
+            // extreme logit over this warp's columns
+            auto publish = [&](int n, int hi, int nu) {
+                const uint32_t sa = tmem + lane_off + (n & 1) * kPpKeys + c0;
+                float e0 = neg ? INFINITY : -INFINITY, e1 = e0;
+#pragma unroll 1
+                for (int hh = 0; hh < nu; ++hh) {
+                    float v[32], w[32];
+                    tmem_ld32(sa + hh * kPpUKeys, v);
+                    tmem_ld32(sa + hh * kPpUKeys + 32, w);
+                    tmem_wait_ld32(v);
+                    tmem_wait_ld32(w);
+                    const int lim = hi - hh * kPpUKeys - c0;
+                    if (__all_sync(0xffffffffu, lim >= 64)) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            e0 = neg ? min3(e0, v[e], v[e + 1]) : max3(e0, v[e], v[e + 1]);
+                            e1 = neg ? min3(e1, w[e], w[e + 1]) : max3(e1, w[e], w[e + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (e < lim) e0 = neg ? fminf(e0, v[e]) : fmaxf(e0, v[e]);
+                            if (e + 32 < lim) e1 = neg ? fminf(e1, w[e]) : fmaxf(e1, w[e]);
+                        }
+                    }
+                }
+                const float ext = neg ? fminf(e0, e1) : fmaxf(e0, e1);
+                xch[((n & 1) * 2 + hw) * 128 + r] = ext;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kPxXch + q4]);
+                return ext;
+            };
             int n = 0;            // S tiles
             uint32_t un = 0;      // P units
             bool ok = true;
@@ -440,119 +461,89 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                     const int nk = pfx_keys(p, it, j);
                     const int key0 = (it.j0 + j) * kPpKeys;
                     const int hi = min(nk, vis - key0);           // valid columns of this row: [0, hi)
-                    const bool live = warp_wait(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag);   // agreed on below
-                    tc_fence_after();
-                    const uint32_t sa = tmem + lane_off + sb * kPpKeys;
                     const int nu = pp_units(nk);
+                    if (!warp_wait(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float ext = publish(n, hi, nu);
+                    if (!warp_wait(&bars[kPxXch + q4], n & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const float other = xch[(sb * 2 + (hw ^ 1)) * 128 + r];
+                    // The reference maximum m of a row is lazy: P = 2^(logit - m) is computed against the reference of
+                    // the earlier tiles, and m moves only when a tile exceeds it by kPxRescale (or the row had none).
+                    const bool fresh = m == -INFINITY;
+                    bool resc = false;
+                    float al = 1.f;
+                    const float dm = hi > 0 ? fmaf(neg ? fminf(ext, other) : fmaxf(ext, other), sl2, fresh ? 0.f : -m) : -INFINITY;
+                    if (fresh ? dm > -INFINITY : dm > kPxRescale) {
+                        const float mn = fresh ? dm : m + dm;
+                        if (!fresh) {
+                            al = ex2(m - mn);
+                            resc = true;
+                        }
+                        m = mn;
+                    }
+                    const bool any = __any_sync(0xffffffffu, resc);
+                    const float mref = m == -INFINITY ? 0.f : m;
+                    const float2 sl = make_float2(sl2, sl2), nm = make_float2(-mref, -mref);
+                    const uint32_t sa = tmem + lane_off + sb * kPpKeys + c0;
                     for (int hh = 0; hh < nu; ++hh, ++un) {
                         const int us = (int)(un % kPpSlots);
-                        const int u_end = hh * kPpUKeys + pp_unit_cols(nk, hh);
-                        const int c_beg = hh * kPpUKeys + 64 * hw;            // this warp's columns
-                        const int c_end = min(c_beg + 64, u_end);             // (may be empty)
-                        // The reference maximum m of a row is lazy: P = 2^(logit - m) is computed
-                        // against the reference of the earlier units, and m moves only when a unit
-                        // exceeds it by kPxRescale -- the unit is then redone against the new reference.
-                        // A quarter in which some row has no reference yet takes the maximum first.
-                        const bool need_max = __any_sync(0xffffffffu, m == -INFINITY && hi > hh * kPpUKeys);
-                        bool resc = false;
-                        float al = 1.f;
-                        if (need_max) {
-                            float tmax = -INFINITY;
-#pragma unroll 1
-                            for (int c0 = c_beg; live && c0 < c_end; c0 += 16) {
-                                float v[16];
-                                tmem_ld16(sa + c0, v);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (c0 + k < hi) tmax = fmaxf(tmax, v[k] * sl2);
-                            }
-                            float tother;
-                            exchange(tmax, &tother);
-                            tmax = fmaxf(tmax, tother);
-                            resc = m != -INFINITY && tmax > m + kPxRescale;
-                            if (resc) al = ex2(m - tmax);
-                            if (resc || (m == -INFINITY && tmax > -INFINITY)) m = tmax;
+                        const int u_cols = pp_unit_cols(nk, hh) - c0;         // columns of this warp (none: <= 0)
+                        const int lim = hi - hh * kPpUKeys - c0;              // valid ones of this row
+                        // slot us of the O rank is free once the PV of unit un - kPpSlots has landed
+                        if (!warp_wait(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1, abort_flag)) {
+                            ok = false;
+                            break;
                         }
-                        // slot us of the O rank is free once the PV of unit un - kPpSlots has landed (a wait that
-                        // ran out is agreed on below: the unit's stores are dropped, its barrier is not armed)
-                        const bool slot = live && warp_wait(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1, abort_flag);
                         // P in bf16 straight into slot us of the O rank: keys 8c..8c+7 of the unit,
                         // this row, at chunk c (2 KB per chunk of 8 keys x 128 rows).  Every store
-                        // counts its bytes on the slot's barrier; each lane quarter arms it once
-                        // it knows how many bytes it stored (a redone unit is stored twice).
+                        // counts its bytes on the slot's barrier, which each lane quarter arms below.
                         const uint32_t pbar = rPFull + us * 8;
                         const uint32_t pbase = rP + us * kPpPBuf;
-                        int attempts = 1;
-                        // columns valid for every row of the warp (most compressed units) skip
-                        // the per-column mask
-                        const bool unmasked = __all_sync(0xffffffffu, hi >= c_end);
-                        float dmax;
-                        // 16 columns from cb: probabilities against mref, stored
-                        auto put16 = [&](auto masked_tag, const float* v, int cb, float2 sl, float2 nm) {
+                        // 16 columns from c
+                        auto put16 = [&](auto masked_tag, const float* v, int c) {
                             constexpr bool kMasked = decltype(masked_tag)::value;
                             uint32_t pk[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 float2 d = fma2(make_float2(v[2 * e], v[2 * e + 1]), sl, nm);
                                 if (kMasked) {
-                                    d.x = cb + 2 * e < hi ? d.x : -INFINITY;
-                                    d.y = cb + 2 * e + 1 < hi ? d.y : -INFINITY;
+                                    d.x = c + 2 * e < lim ? d.x : -INFINITY;
+                                    d.y = c + 2 * e + 1 < lim ? d.y : -INFINITY;
                                 }
-                                dmax = max3(dmax, d.x, d.y);
                                 pk[e] = pack_bf16x2(ex2(d.x), ex2(d.y));
                             }
-                            const uint32_t ra = pbase + ((uint32_t)(cb - hh * kPpUKeys) >> 3) * 2048u;
+                            const uint32_t ra = pbase + (uint32_t)c * 256u;
                             pp_st_async_v4(ra, pk[0], pk[1], pk[2], pk[3], pbar);
                             pp_st_async_v4(ra + 2048u, pk[4], pk[5], pk[6], pk[7], pbar);
                         };
-                        auto pass2 = [&](float mref) {
-                            const float2 sl = make_float2(sl2, sl2), nm = make_float2(-mref, -mref);
-                            dmax = -INFINITY;
-                            if (unmasked && c_end == c_beg + 64) {
-                                // the second half's load runs while the first half is worked on
-                                float v[32], w[32];
-                                tmem_ld32(sa + c_beg, v);
-                                tmem_wait_ld32(v);
-                                tmem_ld32(sa + c_beg + 32, w);
-                                put16(std::false_type{}, v, c_beg, sl, nm);
-                                put16(std::false_type{}, v + 16, c_beg + 16, sl, nm);
-                                tmem_wait_ld32(w);
-                                put16(std::false_type{}, w, c_beg + 32, sl, nm);
-                                put16(std::false_type{}, w + 16, c_beg + 48, sl, nm);
-                            } else {
+                        const uint32_t su = sa + hh * kPpUKeys;
+                        // columns valid for every row of the warp (most units) skip the per-column mask
+                        if (__all_sync(0xffffffffu, lim >= 64)) {
+                            // the second half's load runs while the first half is worked on
+                            float v[32], w[32];
+                            tmem_ld32(su, v);
+                            tmem_wait_ld32(v);
+                            tmem_ld32(su + 32, w);
+                            put16(std::false_type{}, v, 0);
+                            put16(std::false_type{}, v + 16, 16);
+                            tmem_wait_ld32(w);
+                            put16(std::false_type{}, w, 32);
+                            put16(std::false_type{}, w + 16, 48);
+                        } else {
 #pragma unroll 1
-                                for (int c0 = c_beg; c0 < c_end; c0 += 16) {
-                                    float v[16];
-                                    tmem_ld16(sa + c0, v);
-                                    tmem_wait_ld();
-                                    put16(std::true_type{}, v, c0, sl, nm);
-                                }
+                            for (int c = 0; c < min(u_cols, 64); c += 16) {
+                                float v[16];
+                                tmem_ld16(su + c, v);
+                                tmem_wait_ld();
+                                put16(std::true_type{}, v, c);
                             }
-                        };
-                        for (int attempt = 0;; ++attempt) {
-                            if (slot) pass2(m == -INFINITY ? 0.f : m);
-                            // one barrier per pass: a row over its reference, or a wait that ran out?
-                            const bool over = slot && !need_max && !attempt && dmax > kPxRescale;
-                            const float mine = slot ? (over ? dmax : -INFINITY) : NAN;
-                            xch[(xpar * 2 + hw) * 128 + r] = mine;
-                            if (!pair_any(over || !slot)) break;
-                            const float other = xch[(xpar * 2 + (hw ^ 1)) * 128 + r];
-                            xpar ^= 1;
-                            if (__any_sync(0xffffffffu, mine != mine || other != other)) {
-                                ok = false;
-                                break;
-                            }
-                            const float dm = fmaxf(mine, other);
-                            if (!__any_sync(0xffffffffu, dm > kPxRescale)) break;
-                            if (dm > kPxRescale) {
-                                al = ex2(-dm);
-                                m += dm;
-                                resc = true;
-                            }
-                            attempts = 2;
                         }
-                        if (!ok) break;
                         if (hh == nu - 1) {
                             // every TMEM load of this warp from the tile has completed
                             tc_fence_before();
@@ -560,15 +551,13 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             if (lane == 0) px_remote_arrive_relaxed(lead_bars + (kPxSEmpty + sb) * 8);
                         }
                         if (hw == 0) {
-                            // unit header: rescale factor per row, per-quarter flag; then the arm:
-                            // this quarter's P bytes (both warps, every attempt) and header bytes
+                            // unit header: rescale factor per row, per-quarter flag (a tile's first unit has both for the
+                            // tile); then the arm: this quarter's P bytes (both warps) and header bytes
                             const uint32_t hdr = rHdr + us * kPpHdrBytes;
-                            pp_st_async_u32(hdr + r * 4, __float_as_uint(al), pbar);
-                            const bool any = __any_sync(0xffffffffu, resc);
+                            pp_st_async_u32(hdr + r * 4, __float_as_uint(hh ? 1.f : al), pbar);
                             if (lane == 0) {
-                                pp_st_async_u32(hdr + 512 + q4 * 4, any ? 1u : 0u, pbar);
-                                pp_remote_arrive_expect_tx(
-                                    pbar, (uint32_t)attempts * (uint32_t)(u_end - hh * kPpUKeys) * 64u + 32u * 4u + 4u);
+                                pp_st_async_u32(hdr + 512 + q4 * 4, any && !hh ? 1u : 0u, pbar);
+                                pp_remote_arrive_expect_tx(pbar, (uint32_t)u_cols * 64u + 32u * 4u + 4u);
                             }
                             if (j == it.n - 1 && hh == nu - 1) p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] = m;
                         }

@@ -1,0 +1,98 @@
+"""decode_shared at its edges: references that move, keys that are not finite, refusals, the serving loop, and how far off
+QK normalisation may be.
+
+Bound of `reference`: with logits off by at most delta_j for key j, |err| <= sum_j p_j delta_j (|v_j| + sum p|v|) to first order
+(1.2 times that while delta <= 0.1), plus 2^-7 sum p|v| for probabilities of one bf16 term and a sum of rounded ones, plus 2^-16
+of it for fp32 sums, plus the output's own rounding."""
+
+import pytest
+import torch
+
+import compressed_long_context_b200 as hca
+
+bf = torch.bfloat16
+
+
+def done():
+    torch.cuda.synchronize()
+    hca.get_device_error()
+
+
+def check(got, out, tol, extra):
+    err = (got.double() - out).abs()
+    lim = tol + extra * (out.abs() + tol) + 1e-30
+    assert bool((err <= lim).all()), float((err / lim).max())
+
+
+def batch(dev, seed, B, Hq, Np, N, W, L):
+    """Arguments of decode_shared on random inputs: one KV head, blocks of 16, sequences of lengths L."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    rb = lambda *s: torch.randn(s, generator=g, device=dev).to(bf)  # noqa: E731
+    return dict(q=rb(B, Hq, 512), kp=rb(Np, 1, 512), vp=rb(Np, 1, 512), kc=rb(B, N, 1, 512), vc=rb(B, N, 1, 512),
+                kw=rb(B, W, 1, 512), vw=rb(B, W, 1, 512), seqlens=torch.tensor(L, dtype=torch.int32, device=dev), blk=16, W=W,
+                scale=512 ** -0.5)
+
+
+def reference(a, dq_prefix=0.0, dq_own=0.0):
+    """Softmax attention in 64 bits over [prefix, own entries, window] (linear window, one KV head), and its bound.  dq_*: how far
+    (2-norm over the channels) a logit may be off for the rounding of normalised operands."""
+    B, Hq, _ = a["q"].shape
+    norm = a.get("gq") is not None
+    unit = lambda x, g: x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * g.double() if norm else x  # noqa: E731
+    out = torch.zeros(B, Hq, 512, dtype=torch.float64, device=a["q"].device)
+    tol = torch.zeros_like(out)
+    Np = a["kp"].shape[0]
+    for b, L in enumerate(a["seqlens"].tolist()):
+        nc, nw = max(0, (L - a["W"]) // a["blk"]), min(L, a["W"])
+        own, pre = max(0, nc - Np), min(nc, Np)
+        K = unit(torch.cat([a["kp"][:pre, 0], a["kc"][b, :own, 0], a["kw"][b, a["W"] - nw:, 0]]).double(), a.get("gk"))
+        V = torch.cat([a["vp"][:pre, 0], a["vc"][b, :own, 0], a["vw"][b, a["W"] - nw:, 0]]).double()
+        Q = unit(a["q"][b].double(), a.get("gq"))
+        p = torch.softmax(Q @ K.T * a["scale"], -1)
+        # every product is off by the same share of itself at most, with independent signs: 6 times the 2-norm of the bounds
+        # is passed with probability 2 exp(-18)
+        rms = torch.sqrt(Q ** 2 @ (K ** 2).T) * abs(a["scale"])
+        delta = 2.0 ** -18 * (Q.abs() @ K.abs().T) * abs(a["scale"])
+        delta = delta + 6 * torch.cat([rms[:, :pre] * dq_prefix, rms[:, pre:] * dq_own], -1)
+        assert float(delta.max()) <= 0.1
+        mass = p @ V.abs()
+        out[b] = p @ V
+        tol[b] = 1.2 * ((p * delta) @ V.abs() + (p * delta).sum(-1, keepdim=True) * mass) + mass * (2.0 ** -7 + 2.0 ** -16)
+    return out, tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Np,step", [(1100, 3), (1100, 1), (395, 2)])
+def test_references_move(cuda_device, libhca, Np, step):
+    """Logits of half the heads rise by more than 2^32 every `step` units of 128 entries, the other half's fall: a unit that moves
+    a row's reference is followed by units that weigh as much, so P against an older reference would show.  The same bits
+    again and again."""
+    dev = cuda_device
+    a = batch(dev, 3, 5, 64, Np, 8, 40, [16 * (Np + i) + 60 for i in range(5)])
+    axis = torch.zeros(512, device=dev)
+    axis[:256] = 1.0
+    level = (torch.arange(Np, device=dev) // (128 * step)).float()           # 40 log2 units more each
+    per = 40 * 0.6931471805599453 / (256 * a["scale"])
+    a["kp"] = (a["kp"].float() + axis * (level * per)[:, None, None]).to(bf)
+    sign = torch.where(torch.arange(64, device=dev) % 2 == 0, 1.0, -1.0)
+    a["q"] = (a["q"].float() * 0.25 + sign[None, :, None] * axis).to(bf)
+    out, tol = reference(a)
+    got = hca.decode_shared(**a, out_f32=True)
+    done()
+    check(got, out, tol, 2.0 ** -16)
+    again = [hca.decode_shared(**a, out_f32=True) for _ in range(20)]
+    done()
+    assert all(torch.equal(x, got) for x in again)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-(512 ** -0.5), 0.0])
+def test_negative_and_zero_scale(cuda_device, libhca, scale):
+    """Any finite logit scale: with a negative one a row's largest logit is its least product.  The third sequence sees a part of the
+    prefix's last tile, the fourth none of it."""
+    a = batch(cuda_device, 4, 4, 24, 700, 12, 33, [16 * 712 + 33, 16 * 705 + 40, 16 * 650 + 33, 40])
+    a["scale"] = scale
+    out, tol = reference(a)
+    got = hca.decode_shared(**a, out_f32=True)
+    done()
+    check(got, out, tol, 2.0 ** -16)
