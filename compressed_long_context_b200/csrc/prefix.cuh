@@ -17,6 +17,10 @@
 // Why pairs: one SM's 128 x 256 x 512 products take 4096 cycles and read 256 KB of K or V, 64 bytes a cycle, more
 // than L2 delivers to all SMs at once; the pair halves that.  The first MMA issuer of a pair (the leader) waits
 // for both SMs' copies (they count their bytes on the leader's barrier), and its commits arrive at both.
+//
+// Every barrier but kPxXch is arrived at from another SM of the cluster as well, so its waits acquire at cluster scope: what
+// the other SM's copies or warps wrote before is then ordered before what follows, the pair's MMAs among it (CTA scope was
+// 0.3 us of 89 faster).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -322,7 +326,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         if (j == 0) {
                             // Q slab s of this row tile, as soon as the previous row tile's last
                             // MMAs on slab s have completed (not after its whole last tile)
-                            if (!mbar_wait(&bars[kPxQEmpty + s], (qn & 1) ^ 1, abort_flag)) {
+                            if (!pp_wait_cl(&bars[kPxQEmpty + s], (qn & 1) ^ 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -332,7 +336,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                        it.g * p.G, it.b0 + half * p.tpt, 0);
                         }
                         const uint32_t st = kr % kPxRing;
-                        if (!mbar_wait(&bars[kPxEmpty + st], ((kr / kPxRing) & 1) ^ 1, abort_flag)) {
+                        if (!pp_wait_cl(&bars[kPxEmpty + st], ((kr / kPxRing) & 1) ^ 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -355,7 +359,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
             for (PfxPiece it = pfx_piece(p, x_beg, x_end); ok && it.n; it = pfx_piece(p, it.next, x_end), ++item_n) {
                 for (int j = 0; ok && j < it.n; ++j, ++n) {
                     const int sb = n & 1;
-                    if (!warp_wait(&bars[kPxSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                    if (!pp_warp_wait_cl(&bars[kPxSEmpty + sb], ((n >> 1) & 1) ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -366,8 +370,8 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                     for (int s = 0; s < 8; ++s) {
                         const uint32_t st = kr % kPxRing;
                         // Q slab s of this row tile (landed once per item, used by every tile)
-                        if ((j == 0 && !warp_wait(&bars[kPxQFull + s], item_n & 1, abort_flag)) ||
-                            !warp_wait(&bars[kPxFull + st], (kr / kPxRing) & 1, abort_flag)) {
+                        if ((j == 0 && !pp_warp_wait_cl(&bars[kPxQFull + s], item_n & 1, abort_flag)) ||
+                            !pp_warp_wait_cl(&bars[kPxFull + st], (kr / kPxRing) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -462,7 +466,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                     const int key0 = (it.j0 + j) * kPpKeys;
                     const int hi = min(nk, vis - key0);           // valid columns of this row: [0, hi)
                     const int nu = pp_units(nk);
-                    if (!warp_wait(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag)) {
+                    if (!pp_warp_wait_cl(&bars[kPxSFull + sb], (n >> 1) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -496,7 +500,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const int u_cols = pp_unit_cols(nk, hh) - c0;         // columns of this warp (none: <= 0)
                         const int lim = hi - hh * kPpUKeys - c0;              // valid ones of this row
                         // slot us of the O rank is free once the PV of unit un - kPpSlots has landed
-                        if (!warp_wait(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1, abort_flag)) {
+                        if (!pp_warp_wait_cl(&bars[kPxPCons + us], ((un / kPpSlots) & 1) ^ 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -580,7 +584,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         for (int h = 0; ok && h < 2; ++h)
                             for (int u = 0; u < nv; ++u) {
                                 const uint32_t st = vr % kPxRing;
-                                if (!mbar_wait(&bars[kPxEmpty + st], ((vr / kPxRing) & 1) ^ 1, abort_flag)) {
+                                if (!pp_wait_cl(&bars[kPxEmpty + st], ((vr / kPxRing) & 1) ^ 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
@@ -615,8 +619,8 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         const bool first = j == 0 && hh == 0;
                         // both SMs' P has landed (seen, and handed to the async proxy, by their rescale warps) and
                         // their O rows are rescaled
-                        if (!warp_wait(&bars[kPxCorr + us], ph, abort_flag) ||
-                            (first && !warp_wait(&bars[kPxOEmpty], (item_n & 1) ^ 1, abort_flag))) {
+                        if (!pp_warp_wait_cl(&bars[kPxCorr + us], ph, abort_flag) ||
+                            (first && !pp_warp_wait_cl(&bars[kPxOEmpty], (item_n & 1) ^ 1, abort_flag))) {
                             ok = false;
                             break;
                         }
@@ -626,7 +630,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                         for (int h = 0; ok && h < 2; ++h)
                             for (int u = 0; u < nv; ++u) {
                                 const uint32_t st = vr % kPxRing;
-                                if (!warp_wait(&bars[kPxFull + st], (vr / kPxRing) & 1, abort_flag)) {
+                                if (!pp_warp_wait_cl(&bars[kPxFull + st], (vr / kPxRing) & 1, abort_flag)) {
                                     ok = false;
                                     break;
                                 }
@@ -707,7 +711,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                             // a row of this warp moved its reference maximum (never in the first
                             // unit of an item): scale O once the PV of unit un-1 has landed
                             const uint32_t pu = un - 1;
-                            if (!warp_wait(&bars[kPxPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
+                            if (!pp_warp_wait_cl(&bars[kPxPCons + pu % kPpSlots], (pu / kPpSlots) & 1, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -738,7 +742,7 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                 // ---- epilogue: the record (l, O), half of the columns for each of a quarter's two warps.  Each warp stages 32 rows x 128 bytes at a time in
                 // shared memory and writes them with one TMA tensor store (a coalesced box);
                 // per-lane row stores would touch 32 lines per instruction.
-                if (!pair_agree_o(warp_wait(&bars[kPxOFull], item_n & 1, abort_flag))) break;
+                if (!pair_agree_o(pp_warp_wait_cl(&bars[kPxOFull], item_n & 1, abort_flag))) break;
                 tc_fence_after();
                 if (!extra) p.pfx_l[(size_t)(cl + it.rt) * 256 + half * 128 + r] = l;
                 uint8_t* stg = sm + kPpSmStage + (q4 * 2 + extra) * (kPpStageWarp / 2);
