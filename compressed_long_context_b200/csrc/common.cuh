@@ -20,11 +20,15 @@
 
 namespace hca {
 
-// Per-device error word: first error wins (atomicCAS from 0).
+// Per-device error word: the first error wins, but one of a kernel that gave up replaces a bad input's, since the passes
+// that follow go by it (their inputs are then incomplete).
 __device__ unsigned int g_error = 0;
 
+__device__ __forceinline__ bool gave_up(unsigned int code) { return code == HCA_ERR_TIMEOUT || code == HCA_ERR_INTERNAL; }
+
 __device__ __forceinline__ void record_error(unsigned int code) {
-    atomicCAS(&g_error, 0u, code);
+    if (atomicCAS(&g_error, 0u, code) == HCA_ERR_DEVICE_INPUT && gave_up(code))
+        atomicCAS(&g_error, (unsigned int)HCA_ERR_DEVICE_INPUT, code);
 }
 
 // Wall-clock bound of one wait.  Legitimate waits in these kernels last microseconds.  The

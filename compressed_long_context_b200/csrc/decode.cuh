@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (*reinterpret_cast<volatile unsigned int*>(&g_error) == HCA_ERR_TIMEOUT) {
+    if (gave_up(*reinterpret_cast<volatile unsigned int*>(&g_error))) {
         // a split CTA gave up: its records (and the unit ranges) may be stale, so the outputs are
         // marked invalid rather than merged from whatever the workspace holds
         if (live)

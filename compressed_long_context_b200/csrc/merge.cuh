@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(MergeShape<CH>::kThreads) merge_kernel(const M
     const unsigned err = __ldcg(&g_error);
     const int first = __ldcg(p.meta + 2 * u), last = __ldcg(p.meta + 2 * u + 1);
     const int clusters = kPfx ? __ldcg(&p.plan->clusters) : 0;
-    if (err == HCA_ERR_TIMEOUT) {
+    if (gave_up(err)) {
         // a CTA gave up: its records may be stale, so the outputs are marked invalid
 #pragma unroll
         for (int x = 0; x < kMergeHeads; ++x) r[x] = make_float4(NAN, NAN, NAN, NAN);

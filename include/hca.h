@@ -455,8 +455,10 @@ const char* hca_status_string(hca_status_t status);
  * HCA_ERR_INTERNAL otherwise, HCA_ERR_CUDA if the read failed.  An error recorded by work on
  * another stream is never lost: it is either returned or left for the next call.  The word
  * is per device and the read-out slot is shared, so make one such call at a time per device.
- * While the word holds HCA_ERR_TIMEOUT, hca_decode writes NaN to its outputs instead of
- * merging split records that a timed-out kernel may have left incomplete.
+ * The first error recorded is kept, except that HCA_ERR_TIMEOUT and HCA_ERR_INTERNAL replace
+ * HCA_ERR_DEVICE_INPUT.  While the word holds one of those two, hca_decode, hca_decode_quant and
+ * hca_decode_shared write NaN to their outputs instead of merging split records that a kernel
+ * which gave up may have left incomplete.
  */
 hca_status_t hca_get_device_error(hca_stream_t stream);
 
@@ -487,9 +489,10 @@ hca_status_t hca_debug_set_dsa_rows_limit(long long rows);
  *
  * hca_debug_set_wait_limit -- set the current device's wait limit in nanoseconds
  *   (0 restores the default of 1 s).  Affects every later launch on the device.
- * hca_debug_set_drop_slab -- on != 0: every later hca_decode launch on the device never
- *   requests the first key slab of each split CTA, so the wait for it runs out after the
- *   wait limit and the whole decode reports HCA_ERR_TIMEOUT (outputs NaN); 0 turns it off.
+ * hca_debug_set_drop_slab -- on != 0: every later hca_decode, hca_decode_quant and
+ *   hca_decode_shared launch on the device never requests the first key slab of each split
+ *   CTA, so the wait for it runs out after the wait limit and the whole decode reports
+ *   HCA_ERR_TIMEOUT (outputs NaN); 0 turns it off.
  * hca_debug_wait_probe -- queue one CTA that waits on a barrier that can never complete
  *   and so records HCA_ERR_TIMEOUT after the wait limit; nothing else is in flight.
  */
