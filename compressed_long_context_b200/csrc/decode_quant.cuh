@@ -837,7 +837,8 @@ decode_quant_kernel(const QuantParams p, const __grid_constant__ CUtensorMap tm_
                 if (sidx < 64) {
                     const float mo = first ? -INFINITY : m_s[sidx];
                     const float mt = fmaxf(fmaxf(red[sidx], red[64 + sidx]), fmaxf(red[128 + sidx], red[192 + sidx]));
-                    const float mn = fmaxf(mo, mt - shift);
+                    // held finite: keys of logit -inf then weigh nothing beside later ones, and NaN stays in the sums
+                    const float mn = fmaxf(fmaxf(mo, mt - shift), kLowest);
                     al_s[sidx] = first ? 0.f : ex2(mo - mn);
                     m_s[sidx] = mn;
                 }

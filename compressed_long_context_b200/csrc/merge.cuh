@@ -79,6 +79,8 @@ struct MergeParams {
     const SharedPlan* plan;
 };
 
+constexpr float kLowest = -3.402823466e38f;     // the lowest finite reference
+
 template <int CH>
 struct MergeShape {
     static constexpr int kThreads = CH == 32 ? 256 : 128;
@@ -170,7 +172,8 @@ __global__ void __launch_bounds__(MergeShape<CH>::kThreads) merge_kernel(const M
                     r[x] = make_float4(r[x].x * sc, r[x].y * sc, r[x].z * sc, r[x].w * sc);
 #pragma unroll
                     for (int k = 0; k < kChunk; ++k) {
-                        // a record without a visible key (m = -inf) holds nothing: its sums are not used
+                        // a record without a visible key (m = -inf) holds nothing: its sums are not used (one whose
+                        // keys all have logits of -inf or NaN has m = kLowest: it weighs nothing, or makes the row NaN)
                         if (m[k][x] == -INFINITY) continue;
                         const float w = exp2f(m[k][x] - Mn);
                         L[x] = fmaf(w, l[k][x], L[x]);

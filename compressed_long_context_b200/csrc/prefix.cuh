@@ -563,7 +563,9 @@ prefix_kernel(const PrefixParams p, const __grid_constant__ CUtensorMap tm_q,
                                 pp_st_async_u32(hdr + 512 + q4 * 4, any && !hh ? 1u : 0u, pbar);
                                 pp_remote_arrive_expect_tx(pbar, (uint32_t)u_cols * 64u + 32u * 4u + 4u);
                             }
-                            if (j == it.n - 1 && hh == nu - 1) p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] = m;
+                            if (j == it.n - 1 && hh == nu - 1)
+                                p.pfx_m[(size_t)(cl + it.rt) * 256 + half * 128 + r] =
+                                    vis > it.j0 * kPpKeys ? fmaxf(m, kLowest) : -INFINITY;
                         }
                     }
                 }

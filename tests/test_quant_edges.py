@@ -47,3 +47,37 @@ def test_missing_slab_beside_a_bad_length(cuda_device, libhca, op):
     done()
     if op != "decode":
         check(good, out, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,ps", [([16 * 257 + 40], 0), ([16 * 257 + 40] + [16 * 128 + 40] * 400, 0), ([16 * 129 + 40, 16 * 300], 64)])
+def test_nan_key(cuda_device, libhca, lengths, ps):
+    """The last entry of a sequence is the only one of its tile of 128, and its key is NaN (a pooled value that was not finite): the
+    sequence's outputs are NaN, as the softmax is, whichever CTA holds the tile; the others' are right."""
+    args, out, tol = decode_case(cuda_device, 3, lengths, 64, 1, 16, 40, ps=ps)
+    n = (lengths[0] - 40) // 16
+    at = (int(args["page_table"][0, (n - 1) // ps]), (n - 1) % ps) if ps else (0, n - 1)
+    args["kc"].view(torch.uint8)[at[0], at[1], 0, 77] = 0x7f
+    got = hca.decode_quant(**args)
+    done()
+    assert torch.isnan(got[0]).all()
+    check(got[1:], out[1:], tol[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [1, 400])
+def test_shared_key_of_minus_infinity(cuda_device, libhca, B):
+    """The only own entry's key has an infinite channel: heads whose logit becomes -inf leave it out, the others are NaN."""
+    dev = cuda_device
+    args, _, _ = make(dev, 3, [16 * 21 + 50] * B, 20, 8, 1, 16, 50)
+    kc = args["kc"].clone()
+    kc[:, 0, 0, 9] = float("-inf")
+    args["q"][:, ::2, 9], args["q"][:, 1::2, 9] = 1.0, -1.0
+    got = hca.decode_shared(**{**args, "kc": kc}, out_f32=True)
+    done()
+    K, V = (torch.cat([p[None, :, 0].expand(B, -1, -1), w[:, :, 0]], 1).double() for p, w in ((args["kp"], args["kw"]), (args["vp"], args["vw"])))
+    Q = args["q"][:, ::2].double()
+    p = torch.softmax(Q @ K.mT * args["scale"], -1)
+    mass, d = p @ V.abs(), (Q.abs() @ K.abs().mT * args["scale"]).amax(-1, keepdim=True)
+    assert torch.isnan(got[:, 1::2]).all()
+    check(got[:, ::2], p @ V, mass * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16), 2.0 ** -16)
