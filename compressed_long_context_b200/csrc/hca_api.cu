@@ -1178,29 +1178,40 @@ extern "C" hca_status_t hca_read_quant(const void* kc, const void* vc, const voi
 
 namespace {
 
-// The attention pass (decode_quant.cuh) over a cache of codes (E8) or of bf16 entries, a window and a workspace whose
-// arguments have been checked; fills in the launch's parameters (p.sc, p.skip and the plan's are the caller's).
+// Whether the attention pass can count a batch's tiles in 31 bits (entries up to the cache's end, the window's twice, and
+// what a unit's start counts as).
+bool tiles_fit(int B, int Hkv, int W, bool paged, int page_size, int max_pages, int Nmax) {
+    const long long cap = paged ? (long long)max_pages * page_size : (long long)Nmax;
+    const long long unit = (cap + 127) / 128 + 2 * ((W + 127LL) / 128) + hca::kQdStart;
+    return (long long)B * Hkv <= 0x7fffffffLL / unit;
+}
+
+struct AttendMaps {
+    CUtensorMap q, k, v, kw, vw;
+};
+
+// The parameters and tensor maps of the attention pass (decode_quant.cuh) over a cache of codes (E8) or of bf16 entries, a
+// window and a workspace whose arguments have been checked (p.sc, p.skip and the plan's are the caller's).
 template <bool E8>
-hca_status_t attend_pass(hca::QuantParams& p, const void* q, const void* kc, const void* vc, const int* page_table,
-                         int page_size, int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
-                         const float* gq, const float* gk, float eps, uint8_t* ws, const DecodeWs& lay, int nsplit, int grid,
-                         int B, int Hq, int Hkv, int blk, int W, int Nmax, float scale, unsigned flags, cudaStream_t s) {
+hca_status_t attend_setup(hca::QuantParams& p, AttendMaps& m, const void* q, const void* kc, const void* vc, const int* page_table,
+                          int page_size, int max_pages, int num_pages, const void* kw, const void* vw, const int* seqlens,
+                          const float* gq, const float* gk, float eps, uint8_t* ws, const DecodeWs& lay, int nsplit,
+                          int B, int Hq, int Hkv, int blk, int W, int Nmax, float scale, unsigned flags) {
     using namespace hca;
     const bool paged = flags & HCA_PAGED, norm = flags & HCA_QK_NORM;
     const uint64_t hd = (uint64_t)Hkv * kDecD;
-    CUtensorMap tq, tk, tv, tkw, tvw;
-    bool ok = make_tmap_4d(&tq, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
+    bool ok = make_tmap_4d(&m.q, q, kDecD, Hq, B, 1, kDecD, (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, 64, 1, 1);
     const uint64_t rows = paged ? page_size : Nmax, outer = paged ? num_pages : B;
     const uint32_t box = paged ? 64 : 128;
     if (E8) {
-        ok &= make_tmap_4d_u8(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
-        ok &= make_tmap_4d_u8(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+        ok &= make_tmap_4d_u8(&m.k, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
+        ok &= make_tmap_4d_u8(&m.v, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 1, box, 1);
     } else {
-        ok &= make_tmap_4d(&tk, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
-        ok &= make_tmap_4d(&tv, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
+        ok &= make_tmap_4d(&m.k, kc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
+        ok &= make_tmap_4d(&m.v, vc, kDecD, Hkv, rows, outer, kDecD, hd, hd * rows, 64, 1, box, 1);
     }
-    ok &= make_tmap_4d(&tkw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
-    ok &= make_tmap_4d(&tvw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&m.kw, kw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
+    ok &= make_tmap_4d(&m.vw, vw, kDecD, Hkv, W, B, kDecD, hd, hd * W, 64, 1, 128, 1);
     if (!ok) return HCA_ERR_CUDA;
 
     p.seqlens = seqlens;
@@ -1214,11 +1225,16 @@ hca_status_t attend_pass(hca::QuantParams& p, const void* q, const void* kc, con
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.blk = blk; p.W = W; p.Nmax = paged ? 0 : Nmax;
     p.page_size = paged ? page_size : 0; p.max_pages = paged ? max_pages : 0; p.num_pages = paged ? num_pages : 0;
     p.cap = paged ? (int)((long long)max_pages * page_size) : Nmax;     // checked to fit
-    // the kernel counts the batch's tiles in 31 bits
-    if ((long long)B * Hkv * ((p.cap + 127LL) / 128 + 2 * ((W + 127LL) / 128) + kQdStart) > 0x7fffffffLL) return HCA_ERR_INVALID_ARG;
     p.flags = (int)flags; p.nsplit = nsplit;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.eps = eps;
+    return HCA_OK;
+}
+
+template <bool E8>
+hca_status_t attend_launch(const hca::QuantParams& p, const AttendMaps& m, int grid, cudaStream_t s) {
+    using namespace hca;
+    const bool paged = p.flags & HCA_PAGED, norm = p.flags & HCA_QK_NORM;
     using Fn = void (*)(const QuantParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                         const CUtensorMap);
     const Fn fn = norm ? (paged ? decode_quant_kernel<true, true, E8> : decode_quant_kernel<true, false, E8>)
@@ -1235,7 +1251,7 @@ hca_status_t attend_pass(hca::QuantParams& p, const void* q, const void* kc, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.pfx_total > 0 ? 1 : 0;         // beside the prefix pass
-    if (cudaLaunchKernelEx(&cfg, fn, p, tq, tk, tv, tkw, tvw) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, fn, p, m.q, m.k, m.v, m.kw, m.vw) != cudaSuccess) {
         cudaGetLastError();
         return HCA_ERR_CUDA;
     }
@@ -1264,6 +1280,7 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
         !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
         return HCA_ERR_INVALID_ARG;
     if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    if (!tiles_fit(B, Hkv, W, paged, page_size, max_pages, Nmax)) return HCA_ERR_INVALID_ARG;
     if (norm && (!gq || !gk || !aligned16(gq) || !aligned16(gk))) return HCA_ERR_INVALID_ARG;
     if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
     if (vha_u || vha_v) {
@@ -1280,9 +1297,10 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
     QuantParams p = {};
     p.sc = static_cast<const uint16_t*>(scales);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const hca_status_t st = attend_pass<true>(p, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk,
-                                              eps, static_cast<uint8_t*>(workspace), lay, nsplit, nsplit, B, Hq, Hkv, blk, W,
-                                              Nmax, scale, flags, s);
+    AttendMaps maps;
+    hca_status_t st = attend_setup<true>(p, maps, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk,
+                                         eps, static_cast<uint8_t*>(workspace), lay, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags);
+    if (st == HCA_OK) st = attend_launch<true>(p, maps, nsplit, s);
     if (st != HCA_OK) return st;
 
     MergeParams mp = {};
@@ -1302,7 +1320,7 @@ extern "C" hca_status_t hca_decode_quant(const void* q, const void* kc, const vo
 }
 
 // ---------------------------------------------------------------------------------------
-// hca_decode_shared: a batch over one copy of its common prefix (prefix.cuh, decode.cuh, merge.cuh).
+// hca_decode_shared: a batch over one copy of its common prefix (prefix.cuh, decode_quant.cuh, merge.cuh).
 namespace {
 
 // Workspace: the split pass's part, then the prefix records and, for QK normalisation, the normalised queries (with
@@ -1422,6 +1440,7 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         !aligned16(vw) || !aligned16(out) || !aligned16(workspace) || !aligned4(seqlens))
         return HCA_ERR_INVALID_ARG;
     if (!cache_geometry(paged, page_table, page_size, max_pages, num_pages, Nmax)) return HCA_ERR_INVALID_ARG;
+    if (!tiles_fit(B, Hkv, W, paged, page_size, max_pages, Nmax)) return HCA_ERR_INVALID_ARG;
     if (norm && (!gq || !gk || !aligned16(gq) || !aligned16(gk))) return HCA_ERR_INVALID_ARG;
     if (gated && (!gate || !aligned16(gate))) return HCA_ERR_INVALID_ARG;
     if (vha_u || vha_v) {
@@ -1438,7 +1457,11 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
     QuantParams dp = {};
     dp.skip = Np;
     int grid = nsplit;
-    hca_status_t st;
+    // everything of the own pass that can be refused, before the first launch
+    AttendMaps maps;
+    hca_status_t st = attend_setup<false>(dp, maps, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk,
+                                          eps, ws, lay.own, nsplit, B, Hq, Hkv, blk, W, Nmax, scale, flags);
+    if (st != HCA_OK) return st;
 
     int clusters = 0;
     MergeParams mp = {};
@@ -1465,6 +1488,16 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         dp.pfx_total = p.total;
         dp.pfx_max = most;
         dp.plan = reinterpret_cast<SharedPlan*>(ws + 64);
+        const uint64_t hd = (uint64_t)Hkv * kDecD;
+        CUtensorMap tq, tk, tv, tout;
+        bool ok = make_tmap_4d(&tq, norm ? static_cast<const void*>(ws + lay.q_off) : q, kDecD, Hq, B, 1, kDecD,
+                               (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, p.G, p.tpt, 1);
+        ok &= make_tmap_4d(&tk, norm ? static_cast<const void*>(ws + lay.k_off) : kp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1,
+                           kPpKeys / 2, 1);
+        ok &= make_tmap_4d(&tv, vp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, 64, 1);
+        const uint64_t rows = (uint64_t)lay.records * 256;
+        ok &= make_tmap_4d_plain(&tout, ws + lay.o_off, 4, kDecD, rows, 1, 1, kDecD, rows * kDecD, rows * kDecD, 32, 32, 1, 1);
+        if (!ok) return HCA_ERR_CUDA;
         if (norm) {
             PrefixPrepParams pp = {};
             pp.q = static_cast<const __nv_bfloat16*>(q);
@@ -1483,16 +1516,6 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
             prefix_prep_kernel<<<(unsigned)((pp.nq + pp.nk + per_cta - 1) / per_cta), kPrepThreads, 0, s>>>(pp);
             if (cudaGetLastError() != cudaSuccess) return HCA_ERR_CUDA;
         }
-        const uint64_t hd = (uint64_t)Hkv * kDecD;
-        CUtensorMap tq, tk, tv, tout;
-        bool ok = make_tmap_4d(&tq, norm ? static_cast<const void*>(ws + lay.q_off) : q, kDecD, Hq, B, 1, kDecD,
-                               (uint64_t)Hq * kDecD, (uint64_t)B * Hq * kDecD, 64, p.G, p.tpt, 1);
-        ok &= make_tmap_4d(&tk, norm ? static_cast<const void*>(ws + lay.k_off) : kp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1,
-                           kPpKeys / 2, 1);
-        ok &= make_tmap_4d(&tv, vp, kDecD, Hkv, Np, 1, kDecD, hd, hd * Np, 64, 1, 64, 1);
-        const uint64_t rows = (uint64_t)lay.records * 256;
-        ok &= make_tmap_4d_plain(&tout, ws + lay.o_off, 4, kDecD, rows, 1, 1, kDecD, rows * kDecD, rows * kDecD, 32, 32, 1, 1);
-        if (!ok) return HCA_ERR_CUDA;
         st = norm ? launch_prefix<true>(p, clusters, tq, tk, tv, tout, s) : launch_prefix<false>(p, clusters, tq, tk, tv, tout, s);
         if (st != HCA_OK) return st;
         mp.pfx_m = p.pfx_m;
@@ -1505,8 +1528,7 @@ extern "C" hca_status_t hca_decode_shared(const void* q, const void* kp, const v
         mp.plan = dp.plan;
     }
     // the sequences' own entries and windows, beside the prefix pass where there is one
-    st = attend_pass<false>(dp, q, kc, vc, page_table, page_size, max_pages, num_pages, kw, vw, seqlens, gq, gk, eps, ws, lay.own,
-                            nsplit, grid, B, Hq, Hkv, blk, W, Nmax, scale, flags, s);
+    st = attend_launch<false>(dp, maps, grid, s);
     if (st != HCA_OK) return st;
     mp.seqlens = seqlens;
     mp.meta = dp.meta;

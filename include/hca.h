@@ -411,6 +411,8 @@ hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales,
  * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v [Hq, vha_rank] fp32 for the mixing of
  * hca_decode_vha (Hkv == 1), else NULL; gq, gk 16-byte aligned; every other argument, the workspace (hca_decode_workspace_size)
  * and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row: its output is zero.
+ * A batch whose caches hold 2^31 tiles of 128 rows or more (B * Hkv times Nmax, or a row of the page table) is refused
+ * with HCA_ERR_INVALID_ARG.
  * Arithmetic: codes go to the tensor cores as they are; the query and the probabilities are split into
  * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.  Value scales of one sequence that
  * lie more than 2^60 apart may cost the keys of the smaller ones their weight.

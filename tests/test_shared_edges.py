@@ -5,10 +5,13 @@ Bound of `reference`: with logits off by at most delta_j for key j, |err| <= sum
 (1.2 times that while delta <= 0.1), plus 2^-7 sum p|v| for probabilities of one bf16 term and a sum of rounded ones, plus 2^-16
 of it for fp32 sums, plus the output's own rounding."""
 
+import ctypes
+
 import pytest
 import torch
 
 import compressed_long_context_b200 as hca
+from compressed_long_context_b200 import _lib
 
 bf = torch.bfloat16
 
@@ -96,3 +99,35 @@ def test_negative_and_zero_scale(cuda_device, libhca, scale):
     got = hca.decode_shared(**a, out_f32=True)
     done()
     check(got, out, tol, 2.0 ** -16)
+
+
+def test_too_many_tiles_are_refused(libhca):
+    """A batch whose caches hold 2^31 tiles of 128 rows or more is refused before anything is launched."""
+    p = ctypes.c_void_p(16)
+
+    def call(B, Nmax=0, mp=0):
+        paged = _lib.HCA_PAGED if mp else 0
+        a = (p if mp else None, 1 << 20 if mp else 0, mp, mp, p, p, p, None, None, 1e-6, None, None, None, 0, p, p, 1 << 62, B, 64, 1,
+             512, 512, 128, 128)
+        return (libhca.hca_decode_shared(p, p, p, p, p, *a, 4, Nmax, 0.05, paged, None),
+                libhca.hca_decode_quant(p, p, p, p, *a, Nmax, 0.05, paged, None))
+    for args in (dict(B=200, Nmax=0x7fffffff), dict(B=300, mp=2047), dict(B=1 << 24, Nmax=1 << 15)):
+        assert call(**args) == (_lib.HCA_ERR_INVALID_ARG,) * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_a_refusal_leaves_the_workspace(cuda_device, libhca, norm):
+    """... and leaves the caller's workspace alone."""
+    dev, B, Np = cuda_device, 200, 40
+    a = batch(dev, 5, B, 64, Np, 1, 16, [16 * Np + 20] * B)
+    gain = torch.ones(512, device=dev)
+    ws = torch.full((hca.decode_shared_workspace_size(B, 64, 1, 512, Np),), 0x5a, dtype=torch.uint8, device=dev)
+    out = torch.zeros(B, 64, 512, dtype=bf, device=dev)
+    P = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    code = libhca.hca_decode_shared(P(a["q"]), P(a["kp"]), P(a["vp"]), P(a["kc"]), P(a["vc"]), None, 0, 0, 0, P(a["kw"]), P(a["vw"]),
+                                    P(a["seqlens"]), P(gain), P(gain), 1e-6, None, None, None, 0, P(out), P(ws), ws.numel(), B, 64, 1,
+                                    512, 512, 16, 16, Np, 0x7fffffff, 0.05, _lib.HCA_QK_NORM if norm else 0,
+                                    ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    done()
+    assert code == _lib.HCA_ERR_INVALID_ARG and bool((ws == 0x5a).all())
