@@ -20,15 +20,17 @@
 
 namespace hca {
 
-// Per-device error word: the first error wins, but one of a kernel that gave up replaces a bad input's, since the passes
-// that follow go by it (their inputs are then incomplete).
+// Per-device error word: the first bad input is kept, and the code of a kernel that gave up replaces it, since the passes that
+// follow go by it (their inputs are then incomplete).
 __device__ unsigned int g_error = 0;
 
 __device__ __forceinline__ bool gave_up(unsigned int code) { return code == HCA_ERR_TIMEOUT || code == HCA_ERR_INTERNAL; }
 
 __device__ __forceinline__ void record_error(unsigned int code) {
-    if (atomicCAS(&g_error, 0u, code) == HCA_ERR_DEVICE_INPUT && gave_up(code))
-        atomicCAS(&g_error, (unsigned int)HCA_ERR_DEVICE_INPUT, code);
+    if (gave_up(code))
+        atomicExch(&g_error, code);
+    else
+        atomicCAS(&g_error, 0u, code);
 }
 
 // Wall-clock bound of one wait.  Legitimate waits in these kernels last microseconds.  The

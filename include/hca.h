@@ -457,8 +457,8 @@ const char* hca_status_string(hca_status_t status);
  * HCA_ERR_INTERNAL otherwise, HCA_ERR_CUDA if the read failed.  An error recorded by work on
  * another stream is never lost: it is either returned or left for the next call.  The word
  * is per device and the read-out slot is shared, so make one such call at a time per device.
- * The first error recorded is kept, except that HCA_ERR_TIMEOUT and HCA_ERR_INTERNAL replace
- * HCA_ERR_DEVICE_INPUT.  While the word holds one of those two, hca_decode, hca_decode_quant and
+ * HCA_ERR_TIMEOUT and HCA_ERR_INTERNAL replace what was recorded before; HCA_ERR_DEVICE_INPUT does
+ * not.  While the word holds one of those two, hca_decode, hca_decode_quant and
  * hca_decode_shared write NaN to their outputs instead of merging split records that a kernel
  * which gave up may have left incomplete.
  */
