@@ -8,7 +8,8 @@
 // x / 2^e and code * 2^e are exact.  The step is 2^-3 of the power of two below |x| (half a step is at
 // most 2^-4 of |x|) down to 2^-6 * 2^e, and 2^-9 * 2^e below; 2^-6 * 2^e is at most 2^-13.8 of max|x|.
 // e4m3 has no infinity: a value that is not finite becomes the NaN code, and takes no part in the
-// maximum.  The clamp at 2^-64 bounds the sums of decode_quant.cuh, which carry 1 / scale.
+// maximum.  At 2^120 codes end at 240, since 256 * 2^120 is more than bf16 and fp32 hold (bf16's largest
+// value, 255 * 2^120, is 2^-4 of itself off then).  The clamp at 2^-64 bounds the sums of decode_quant.cuh, which carry 1 / scale.
 #pragma once
 
 #include "common.cuh"
@@ -79,8 +80,14 @@ __device__ __forceinline__ uint32_t q_split(float a, float b, uint32_t& rest) {
 // every finite x that took part in the maximum.)
 __device__ __forceinline__ float q_prep(float x, float inv) { return fabsf(x) < INFINITY ? x * inv : NAN; }
 
+// Codes of entries' values, held where their value is finite in bf16.
+constexpr float kQTop = 0x1.ep+127f;                    // 240 * 2^120
+__device__ __forceinline__ float q_hold(float x, float inv) {
+    return q_prep(fabsf(x) < INFINITY ? fminf(fmaxf(x, -kQTop), kQTop) : x, inv);
+}
+__device__ __forceinline__ uint32_t q_codes2(float a, float b, float inv) { return cvt_e4m3x2(q_hold(a, inv), q_hold(b, inv)); }
 __device__ __forceinline__ uint32_t q_codes4(float4 x, float inv) {
-    return cvt_e4m3x2(q_prep(x.x, inv), q_prep(x.y, inv)) | cvt_e4m3x2(q_prep(x.z, inv), q_prep(x.w, inv)) << 16;
+    return q_codes2(x.x, x.y, inv) | q_codes2(x.z, x.w, inv) << 16;
 }
 
 // ------------------------------------------------------------------ tcgen05, kind::f8f6f4

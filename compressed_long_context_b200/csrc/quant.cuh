@@ -139,7 +139,7 @@ __device__ __forceinline__ void pool_rows_quant(const __nv_bfloat16* __restrict_
     }
     const uint32_t byte = q_scale_byte(block_amax<THREADS>(fmaxf(q_mag(s0), q_mag(s1)), scratch));
     const float inv = q_inv_scale(byte);
-    if (mine) reinterpret_cast<uint16_t*>(dst)[tid] = (uint16_t)cvt_e4m3x2(q_prep(s0, inv), q_prep(s1, inv));
+    if (mine) reinterpret_cast<uint16_t*>(dst)[tid] = (uint16_t)q_codes2(s0, s1, inv);
     if (tid == 0) *scale = (uint8_t)byte;
 }
 

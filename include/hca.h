@@ -372,7 +372,8 @@ hca_status_t hca_gate_logits(const void* cq, const void* wg, void* gate, int n, 
  * The value of a code c is c * 2^e.  e is the smallest integer with max|x| <= 448 * 2^e over the vector,
  * clamped to [-64, 120]; the maximum is over finite values, and a value that is not finite is stored
  * as NaN.  Codes are rounded to nearest even from the fp32 pooled entry (one rounding): off by at most
- * max(2^-4 |x|, 2^(e - 10)).  Readers accept the scales these calls write: powers of two in that range.
+ * max(2^-4 |x|, 2^(e - 10)); at e = 120 the largest code is 240, so that every value is finite in bf16.
+ * Readers accept the scales these calls write: powers of two in that range.
  *
  * hca_compress_quant -- hca_compress into the 8-bit form.  k, v, w as for hca_compress;
  *   kc [B,Nc,Hkv,d], vc [B,Nc,Hkv,dv] codes (16-byte aligned), scales [B,Nc,Hkv,2] (2-byte aligned).
@@ -385,7 +386,9 @@ hca_status_t hca_compress_quant(const void* k, const void* v, const float* w, vo
  * hca_append_quant -- hca_append into the 8-bit form: the newest token enters the bf16 window ring and
  * the fp32 pool; a block it completes becomes one 8-bit entry.  kc, vc, scales: [B,Nmax,Hkv,..], or page
  * pools [P,page_size,Hkv,..] with HCA_PAGED; the state (hca_append_state_size) and every other argument
- * as for hca_append.  seqlens[b] == 0 marks a padding row: nothing of it is read or written.
+ * as for hca_append.  seqlens[b] == 0 marks a padding row: nothing of it is written.
+ * The pool sums exp(w_i - max w) x_i in fp32: a block whose sum leaves fp32's range (128 equal weights on values of 2^121)
+ * ends as NaN, where hca_compress_quant's mean of it is finite.
  */
 hca_status_t hca_append_quant(const void* k_new, const void* v_new, const float* w_new, const int* seqlens,
                               void* kw, void* vw, void* kc, void* vc, void* scales,

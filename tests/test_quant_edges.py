@@ -81,3 +81,60 @@ def test_shared_key_of_minus_infinity(cuda_device, libhca, B):
     mass, d = p @ V.abs(), (Q.abs() @ K.abs().mT * args["scale"]).amax(-1, keepdim=True)
     assert torch.isnan(got[:, 1::2]).all()
     check(got[:, ::2], p @ V, mass * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16), 2.0 ** -16)
+
+
+def appended(k, w, blk):
+    """(kc, sc) of the single sequence k [T, d], appended token by token as keys and values."""
+    T, d = k.shape
+    dev = k.device
+    kw = torch.zeros(1, 4, 1, d, dtype=bf, device=dev)
+    vw, vc = torch.zeros_like(kw), torch.zeros(1, T // blk, 1, d, dtype=torch.uint8, device=dev).view(f8)
+    kc, sc = torch.zeros_like(vc.view(torch.uint8)).view(f8), torch.zeros(1, T // blk, 1, 2, dtype=torch.uint8, device=dev).view(e8)
+    st = torch.zeros(hca.append_state_size(1, 1, d, d), dtype=torch.uint8, device=dev)
+    for t in range(T):
+        x = k[t].view(1, 1, d)
+        hca.append_quant(x, x.clone(), None if w is None else w[t:t + 1], torch.tensor([t + 1], dtype=torch.int32, device=dev), kw, vw,
+                         kc, vc, sc, st, blk)
+    assert torch.equal(kc.view(torch.uint8), vc.view(torch.uint8))
+    return kc, sc
+
+
+@pytest.mark.gpu
+def test_largest_values_read_back(cuda_device, libhca):
+    """Values up to bf16's largest, written at once or appended: entries read back finite, and 2^-4 of themselves off at most
+    (the pooling: far less than 2^-12)."""
+    dev = cuda_device
+    top = torch.finfo(bf).max
+    # each row's own largest value: below and above 248 * 2^120, where a code would round to 256
+    mags = torch.tensor([top, 254 * 2.0 ** 120, 248 * 2.0 ** 120, 247 * 2.0 ** 120, 232 * 2.0 ** 120, 2.0 ** 127, 448 * 2.0 ** 119,
+                         2.0 ** 100], device=dev)
+    x = mags[:, None].expand(8, 64).clone()
+    x[:, 1::2] *= -1
+    x[:, 2::4] *= 0.37
+    x = x.to(bf)
+    for blk in (1, 5):
+        rows = x.repeat_interleave(blk, 0)
+        k = rows.view(1, -1, 1, 64)
+        cases = [hca.compress_quant(k, k, blk=blk)]
+        if blk == 1:
+            kc, sc = appended(rows, None, blk)
+            cases.append((kc, kc, sc))
+        for kc, vc, sc in cases:
+            back = hca.read_quant(kc, vc, sc, torch.tensor([8], dtype=torch.int32, device=dev), 8)
+            done()
+            for b in back:
+                got, want = b[0, :, 0].double(), x.double()
+                assert bool(torch.isfinite(got).all())
+                assert bool(((got - want).abs() <= (2.0 ** -4 + 2.0 ** -12) * want.abs()).all())
+
+
+@pytest.mark.gpu
+def test_append_of_large_values(cuda_device, libhca):
+    """128 tokens of 2^120 with equal weights are within the pool's range: the entry of the whole prompt."""
+    dev, blk = cuda_device, 128
+    x = torch.full((blk, 64), 2.0 ** 120, device=dev).to(bf)
+    x[:, ::3] = -1.5 * 2.0 ** 119
+    a = hca.compress_quant(x.view(1, blk, 1, 64), x.view(1, blk, 1, 64), blk=blk)
+    kc, sc = appended(x, torch.full((blk,), 0.25, device=dev), blk)
+    done()
+    assert torch.equal(kc.view(torch.uint8), a[0].view(torch.uint8)) and torch.equal(sc.view(torch.uint8), a[2].view(torch.uint8))
