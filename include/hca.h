@@ -418,7 +418,8 @@ hca_status_t hca_read_quant(const void* kc, const void* vc, const void* scales,
  * with HCA_ERR_INVALID_ARG.
  * Arithmetic: codes go to the tensor cores as they are; the query and the probabilities are split into
  * two 8-bit terms each (bf16 precision); fp32 accumulation and softmax.  Value scales of one sequence that
- * lie more than 2^60 apart may cost the keys of the smaller ones their weight.
+ * lie more than 2^100 apart may cost the keys of the smaller ones their weight (a key's probability times its value's scale is
+ * held in fp32, from 2^8 of the row's largest down to 2^-126).
  */
 hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, const void* scales,
                               const int* page_table, int page_size, int max_pages, int num_pages,

@@ -138,3 +138,23 @@ def test_append_of_large_values(cuda_device, libhca):
     kc, sc = appended(x, torch.full((blk,), 0.25, device=dev), blk)
     done()
     assert torch.equal(kc.view(torch.uint8), a[0].view(torch.uint8)) and torch.equal(sc.view(torch.uint8), a[2].view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", [0, 1])
+def test_value_scales_far_apart(cuda_device, libhca, order):
+    """Value scales 2^100 apart, in tiles of their own: every key keeps its weight in the others' sums."""
+    dev = cuda_device
+    args, _, _ = decode_case(dev, 7, [16 * 512 + 40] * 160, 64, 1, 16, 40)
+    sc = args["sc"].view(torch.uint8)
+    small = (torch.arange(512, device=dev) // 128) % 2 == order
+    sc[:, :, 0, 1] = torch.where(small, 127 - 40, 127 + 60).to(torch.uint8)
+    got = hca.decode_quant(**args, out_f32=True)
+    done()
+    for b in (0, 77, 159):
+        val = lambda c, i: c[b, :, 0].float().double() * torch.pow(2.0, sc[b, :, 0, i:i + 1].double() - 127)  # noqa: E731
+        K, V = (torch.cat([val(args[n], i), args[w][b, :, 0].double()]) for i, (n, w) in enumerate((("kc", "kw"), ("vc", "vw"))))
+        Q = args["q"][b].double()
+        p = torch.softmax(Q @ K.T * args["scale"], -1)
+        d = (Q.abs() @ K.abs().T * args["scale"]).amax(-1, keepdim=True)
+        check(got[b], p @ V, (p @ V.abs()) * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16), 2.0 ** -16)
