@@ -158,3 +158,126 @@ def test_value_scales_far_apart(cuda_device, libhca, order):
         p = torch.softmax(Q @ K.T * args["scale"], -1)
         d = (Q.abs() @ K.abs().T * args["scale"]).amax(-1, keepdim=True)
         check(got[b], p @ V, (p @ V.abs()) * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16), 2.0 ** -16)
+
+
+# ------------------------------------------------------------------ QK normalisation, as exactly as it is held
+#
+# One-hot values, so that an output is a key's probability.  A logit is a sum of 512 products, each off by a share of itself with
+# its own sign: 6 times the 2-norm of the bounds is passed with probability 2 exp(-18), and the root mean square of a rounding is
+# at most its bound / sqrt(3).  One probability is off by p_j (delta_j + sum p delta) to first order (1.2 times while delta <=
+# 0.1); over all keys the root mean square counts delta_j and the row's mean as if they were independent, at most: twice the square.
+
+def heads_and_keys(args, b, keys):
+    """q / rms(q) * gq * gk of the heads and k / rms(k) of the keys, in 64 bits."""
+    unit = lambda x: x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6)  # noqa: E731
+    return unit(args["q"][b].double()) * (args["gq"] * args["gk"]).double(), unit(keys.double())
+
+
+def rounded(Q, K, scale, rel, low=0.0):
+    """(2-norm, 1-norm) bounds of the logits for products off by `rel` of themselves, and queries off by `low` of their largest."""
+    two = rel ** 2 * (Q ** 2 @ (K ** 2).T)
+    if low:
+        two = two + (low * Q.abs().amax(-1, keepdim=True)) ** 2 * (K ** 2).sum(-1)
+    return torch.sqrt(two) * scale, 2.0 ** -18 * (Q.abs() @ K.abs().T) * scale
+
+
+def two_terms(Q, lo=True):
+    """The query as two e4m3 terms, scaled so that its largest value lies in (224, 448]."""
+    e = torch.ceil(torch.log2(Q.abs().amax(-1, keepdim=True) / 448))
+    x = Q * torch.pow(2.0, -e)
+    hi = x.float().to(f8).double()
+    return (hi + ((x - hi).float().to(f8).double() if lo else 0)) * torch.pow(2.0, e)
+
+
+QUANT_REL, QUANT_LOW = 2.0 ** -8 + 2.0 ** -11, 2.0 ** -10 / 224      # e4m3 of e4m3's rest, from fp16; below its normal range
+
+
+def quant_norm_case(dev):
+    """A sequence of 400 8-bit entries and a window of 60, QK normalisation: (args, keys, probabilities, bounds)."""
+    args, out, _ = decode_case(dev, 9, [16 * 400 + 60], 64, 1, 16, 60, norm=True, onehot=True)
+    sc = args["sc"].view(torch.uint8)[0, :, 0].double() - 127
+    K = torch.cat([args["kc"][0, :, 0].float().double() * torch.pow(2.0, sc[:, :1]), args["kw"][0, :, 0].double()])
+    Q, K = heads_and_keys(args, 0, K)
+    p = torch.softmax(Q @ K.T * args["scale"], -1)
+    v = torch.cat([torch.pow(2.0, sc[:, 1]), torch.ones(60, dtype=torch.float64, device=sc.device)])      # the one-hot values
+    two, one = rounded(Q, K, args["scale"], QUANT_REL, QUANT_LOW)
+    return args, Q, K, p, v, two, one
+
+
+def quant_norm_check(got, p, v, two, one):
+    """got [heads, keys]: probabilities times values."""
+    delta = 6 * two + one
+    assert float(delta.max()) <= 0.1
+    lost = 2.0 ** -17 * (p * v).amax(-1, keepdim=True)                    # p held in two 8-bit terms (a code of 1 per key)
+    tol = 1.2 * (p * delta + (p * delta).sum(-1, keepdim=True) * p) * v + p * v * (2.0 ** -7 + 2.0 ** -16) + lost
+    err = (got - p * v).abs()
+    # 2-norm: 2^-7 / sqrt(3) for the two terms of p, and what keys lose whose value lies far below the row's largest (a key 2^30
+    # below, as here, has p v below 2^-17 of the row's largest altogether and may be lost whole: 2^-17 max(p v) >= p v)
+    limit = torch.sqrt(((p * v) ** 2 * (2 * two ** 2 / 3 + 2.0 ** -14 / 3) + lost ** 2).sum())
+    rms = torch.sqrt((err ** 2).sum())
+    return float((err / tol).max()), float(rms / limit)
+
+
+def of_channels(got, n, w):
+    """[heads, keys] of one-hot outputs: entry j in channel j, window slot i in channel 511 - i."""
+    return torch.cat([got[:, :n], got[:, 512 - w:].flip(-1)], -1).double()
+
+
+def test_norm_bound_sees_the_low_term():
+    """The bound holds for the query as the kernel keeps it, and not without its low term."""
+    args, Q, K, p, v, two, one = quant_norm_case(torch.device("cpu"))
+    both, high = (quant_norm_check(torch.softmax(two_terms(Q, lo) @ K.T * args["scale"], -1) * v, p, v, two, one) for lo in (True, False))
+    assert both[0] <= 1 and both[1] <= 1
+    assert high[0] > 1 and high[1] > 2
+
+
+@pytest.mark.gpu
+def test_norm_query_is_held_in_eight_bits(cuda_device, libhca):
+    args, Q, K, p, v, two, one = quant_norm_case(cuda_device)
+    got = hca.decode_quant(**args, out_f32=True)
+    done()
+    worst, rms = quant_norm_check(of_channels(got[0], 400, 60), p, v, two, one)
+    assert worst <= 1 and rms <= 1, (worst, rms)
+
+
+SHARED_REL = 2.0 ** -10.5                                             # fp16 queries and keys: 2^-11 each
+
+
+def shared_norm_case(dev):
+    """Two sequences wholly behind a prefix of 400 entries, QK normalisation: (args, [Q, K, p, 2-norm, 1-norm] of each)."""
+    args, _, _ = make(dev, 8, [16 * 402 + 40, 16 * 401 + 40], 400, 64, 1, 16, 40, norm=True, onehot=True)
+    rows = []
+    for b in range(2):
+        Q, K = heads_and_keys(args, b, torch.cat([args["kp"][:, 0], args["kc"][b, :2 - b, 0], args["kw"][b, :, 0]]))
+        rows.append((Q, K, torch.softmax(Q @ K.T * args["scale"], -1)) + rounded(Q, K, args["scale"], SHARED_REL))
+    return args, rows
+
+
+def shared_norm_check(got, p, two):
+    """got [heads, prefix keys]: their probabilities, each rounded to bf16 (2^-8 / sqrt(3)); the part of the others in the sum is off
+    by their own 2^-8, which all of a row share."""
+    n = got.shape[-1]
+    err = ((got - p[:, :n]) ** 2).sum()
+    limit = (p[:, :n] ** 2 * (2 * two[:, :n] ** 2 / 3 + 2.0 ** -16 / 3 + (2.0 ** -8 * p[:, n:].sum(-1, keepdim=True)) ** 2)).sum()
+    return float(torch.sqrt(err / limit))
+
+
+def test_norm_bound_sees_sixteen_bit_operands():
+    """The bound holds for fp16 queries and keys and P in bf16, and not for bf16 queries and keys."""
+    args, rows = shared_norm_case(torch.device("cpu"))
+    for Q, K, p, two, _ in rows:
+        def sim(t):
+            z = (Q.to(t).double() @ K.to(t).double().T) * args["scale"]
+            e = torch.exp(z - z.amax(-1, keepdim=True)).to(bf).double()
+            return (e / e.sum(-1, keepdim=True))[:, :400]
+        assert shared_norm_check(sim(torch.float16), p, two) <= 1 < shared_norm_check(sim(bf), p, two)
+
+
+@pytest.mark.gpu
+def test_norm_prefix_is_held_in_eleven_bits(cuda_device, libhca):
+    args, rows = shared_norm_case(cuda_device)
+    got = hca.decode_shared(**args, out_f32=True)
+    done()
+    for b, (_, _, p, two, _) in enumerate(rows):
+        rel = shared_norm_check(got[b, :, :400].double(), p, two)
+        assert rel <= 1, rel
