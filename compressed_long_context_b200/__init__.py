@@ -599,7 +599,9 @@ def decode_shared(q, kp, vp, kc, vc, kw, vw, seqlens, blk, W, scale, page_table=
     """``decode`` of a batch whose sequences begin with the same compressed entries, held once and attended
     once for all: kp / vp [Np,Hkv,512] bf16.  kc / vc hold each sequence's entries from the Np-th on (contiguous
     [B,Nmax,Hkv,512], or page pools with page_table); seqlens count the prefix's tokens too.  Other arguments
-    as for ``decode``.  Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero."""
+    as for ``decode``.  Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero.
+    While serving, ``append`` into kc / vc takes the lengths behind the prefix, seqlens - Np * blk, and the window ring
+    (window_ring=True) begins with the prefix's last W tokens, position p in slot (p - Np * blk) % W; Np * blk >= W."""
     _need(q, _BF16, "q")
     dev = q.device
     B, Hq, d = q.shape

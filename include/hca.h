@@ -439,6 +439,10 @@ hca_status_t hca_decode_quant(const void* q, const void* kc, const void* vc, con
  * out [B,Hq,dv] bf16, or fp32 with HCA_OUT_F32; vha_u, vha_v, gq, gk as for hca_decode_quant;
  * every other argument and the supported shapes as for hca_decode.  seqlens[b] == 0 marks a padding row:
  * its output is zero.  The prefix's entries are finite: one that is not may reach sequences that do not see it.
+ * Serving: hca_append keeps a sequence's own cache when it is given the lengths behind the prefix, seqlens[b] - Np * blk with
+ * the new token counted, and a pooling state that was zero at the prefix's end; this call takes the full lengths, and
+ * HCA_WINDOW_RING.  Position p then lies in window slot (p - Np * blk) mod W, which is slot p % W where W divides Np * blk: fill
+ * the ring with the prefix's last W tokens in that order.  Np * blk >= W, so that the ring is full from the first token on.
  * The workspace: hca_decode_shared_workspace_size bytes.
  */
 size_t hca_decode_shared_workspace_size(int B, int Hq, int Hkv, int dv, int Np);

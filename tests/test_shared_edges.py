@@ -131,3 +131,54 @@ def test_a_refusal_leaves_the_workspace(cuda_device, libhca, norm):
                                     ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     done()
     assert code == _lib.HCA_ERR_INVALID_ARG and bool((ws == 0x5a).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,ps", [(40, 0), (32, 64)])
+def test_serving_on_a_shared_prefix(cuda_device, libhca, W, ps):
+    """Token after token: append with the lengths behind the prefix, decode_shared with the full ones.  Every step against 64
+    bits, and the same sequences through append and decode on caches of their own."""
+    dev, blk, P, B, steps = cuda_device, 16, 20, 3, 130
+    g = torch.Generator(device=dev).manual_seed(2)
+    n0 = P * blk
+    rb = lambda *s: torch.randn(s, generator=g, device=dev).to(bf)  # noqa: E731
+    k, v, q = (torch.cat([rb(1, n0, 1, 512).expand(B, -1, -1, -1), rb(B, steps, 1, 512)], 1).contiguous() for _ in range(3))
+    kp, vp = (t[0] for t in hca.compress(k[:1, :n0].contiguous(), v[:1, :n0].contiguous(), blk=blk))
+    N = steps // blk + 1
+    zeros = lambda *s: torch.zeros(s, dtype=bf, device=dev)  # noqa: E731
+    state = lambda: torch.zeros(hca.append_state_size(B, 1, 512, 512), dtype=torch.uint8, device=dev)  # noqa: E731
+    # on the shared prefix: position p in slot (p - n0) % W
+    table = torch.randperm(B, generator=torch.Generator().manual_seed(1)).view(B, 1).to(torch.int32).to(dev) if ps else None
+    kc, vc = (zeros(B, ps or N, 1, 512) for _ in range(2))
+    kw, vw = (x[:, n0 - W:n0].contiguous() for x in (k, v))       # position n0 - W + i is in slot i
+    st = state()
+    # on caches of their own: position p in slot p % W
+    full = [torch.cat([p[None].expand(B, -1, -1, -1), zeros(B, N, 1, 512)], 1).contiguous() for p in (kp, vp)]
+    ring = [x[:, n0 - W:n0].roll(n0 % W, 1).contiguous() for x in (k, v)]
+    st2 = state()
+    seq = torch.full((B,), n0, dtype=torch.int32, device=dev)
+    one = [torch.cat([p[None].expand(B, -1, -1, -1), hca.compress(*(x[:, n0:].contiguous() for x in (k, v)), blk=blk)[i]], 1)[:, :, 0]
+           for i, p in enumerate((kp, vp))]
+    for t in range(n0, n0 + steps):
+        seq += 1
+        kn, vn, qn = k[:, t].contiguous(), v[:, t].contiguous(), rb(B, 64, 512)
+        hca.append(kn, vn, None, seq - n0, kw, vw, kc, vc, st, blk, page_table=table)
+        hca.append(kn, vn, None, seq, ring[0], ring[1], full[0], full[1], st2, blk)
+        if t % 7 and t < n0 + steps - 3:
+            continue
+        got = hca.decode_shared(qn, kp, vp, kc, vc, kw, vw, seq, blk, W, 512 ** -0.5, page_table=table, window_ring=True, out_f32=True)
+        ref = hca.decode(qn, full[0], full[1], ring[0], ring[1], seq, blk, W, 512 ** -0.5, window_ring=True)
+        done()
+        nc = (t + 1 - W) // blk
+        for b in range(B):
+            # entries appended differ from the prompt's by a bf16 step at most: 2^-7 of them, in keys and values
+            K = torch.cat([one[0][b, :nc], k[b, t + 1 - W:t + 1, 0]]).double()
+            V = torch.cat([one[1][b, :nc], v[b, t + 1 - W:t + 1, 0]]).double()
+            Q = qn[b].double()
+            p = torch.softmax(Q @ K.T * 512 ** -0.5, -1)
+            mass, d = p @ V.abs(), (Q.abs() @ K.abs().T * 512 ** -0.5).amax(-1, keepdim=True)
+            own = p[:, P:max(P, nc)]
+            step = 2.0 ** -7 * (own @ V[P:max(P, nc)].abs())
+            moved = 2.0 ** -7 * torch.einsum("hn,hn->h", own, Q.abs() @ K[P:max(P, nc)].abs().T * 512 ** -0.5)[:, None] * 2 * mass
+            for x in (got[b], ref[b]):
+                check(x, p @ V, mass * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16) + step + 1.2 * moved, 2.0 ** -16)
