@@ -1065,15 +1065,19 @@ hca_status_t launch_merge_as(const hca::MergeParams& mp, bool prefix, cudaStream
     return HCA_OK;
 }
 
-// The merge pass after the passes that wrote the records; it may start while they still run.  Records per round go by the
-// average number of pieces per unit, nsplit / U: many pieces, eight (one sequence of 1M tokens, 65 pieces: 25.6
-// against 32.0 us with four and fewer CTAs) or four (16 of
-// 512K: 35.1 against 35.8 us with two), few, two (64 of 128K: 38.5 against 39.5 us with four).  Few units also take
-// channels eight at a time, for more CTAs than SMs.
+// The merge pass after the passes that wrote the records.  Records per round and channels per CTA go by the number of units
+// (sequence, KV head), which bounds a unit's pieces: at most SMs / units and a few, of the own pass and of the prefix.
+//   up to SMs / 16 units: eight records, eight channels (more CTAs than SMs).  One sequence of 1M tokens (65 pieces): 25.6
+//     against 32.0 us with four and 32; decode_shared, one or four sequences on 8191 entries: 28.6 and 29.6 against 32.7 us
+//     (with one piece, on 32 entries, 21.3 against 21.3 with two and 32);
+//   up to SMs / 8: four records, 32 channels.  16 of 128K: 22.5 against 23.1 us with two and 24.6 with eight; decode_shared, 16
+//     on 8191 entries: 39.0 against 39.3 and 41.2 us (on 32 entries 23.8 against 23.3 with two);
+//   more: two records.  32 of 128K: 30.5 against 31.1 us with four, 64: 40.5 against 42.5; decode_shared, 32 on 32, 1023 and 8191
+//     entries: 25.6, 32.1 and 54.1 against 27.8, 34.4 and 55.5 us, 64 on 8191: 84.2 against 87.2.
 hca_status_t launch_merge(const hca::MergeParams& mp, bool prefix, cudaStream_t s) {
     const long long U = (long long)mp.B * mp.Hkv;
     if (16 * U <= mp.nsplit) return launch_merge_as<8, 8>(mp, prefix, s);
-    if (3 * U <= mp.nsplit) return launch_merge_as<4, 32>(mp, prefix, s);
+    if (8 * U <= mp.nsplit) return launch_merge_as<4, 32>(mp, prefix, s);
     return launch_merge_as<2, 32>(mp, prefix, s);
 }
 
