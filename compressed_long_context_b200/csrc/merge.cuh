@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(MergeShape<CH>::kThreads) merge_kernel(const M
     float* ts = os + kDecHeads * CH;                  // [R][CH]  V^T o
     float* vs = ts + R * CH;                          // [G][R]
     float* us = vs + kDecHeads * R;                   // [G][R]
-    // the inputs are not products of the passes before: read while those still run
+    // the inputs are not products of the passes before: read ahead of the wait for their last writes (this grid starts when
+    // their CTAs have left)
     uint2 graw[kMergeHeads];
 #pragma unroll
     for (int x = 0; x < kMergeHeads; ++x) {

@@ -61,7 +61,7 @@ __device__ __forceinline__ PfxPiece pfx_piece(const PrefixParams& p, long long x
 __device__ __forceinline__ int pfx_keys(const PrefixParams& p, const PfxPiece& it, int j) {
     return min(kPpKeys, p.Np - kPpKeys * (it.j0 + j));
 }
-// Tiles of 128 keys of a sequence's own entries and window (as q_unit of decode_quant.cuh counts them).
+// Tiles of 128 keys of a sequence's own entries and window (as q_keys_of and q_tiles of decode_quant.cuh count them).
 __device__ __forceinline__ long long own_tiles(int L, int W, int blk, int Np, long long cap) {
     L = max(L, 1);
     const long long a = (long long)L - W, n0 = a > 0 ? a / blk : 0;

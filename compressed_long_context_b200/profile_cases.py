@@ -151,7 +151,7 @@ def run(case: str, reps: int, B_override: int = 0, L_override: int = 0, T_overri
             dsa_attend(inp["q"], inp["k"], inp["v"], idx, inp["seqlens"], 1 / math.sqrt(cfg.d), out=out)
         nbytes = cfg.B * cfg.L * (cfg.dI * 2 + 8) + cfg.B * cfg.topk * (4 * cfg.d + 8)
     elif case in ("compress_quant", "read_quant", "decode_quant"):
-        # 2 sequences x 131072 tokens pooled into 8-bit entries; 64 sequences of 128K tokens read back and decoded
+        # 2 sequences x 131072 tokens pooled into 8-bit entries; 256 sequences of 128K tokens read back and decoded
         d, W = 512, 128
         if case == "compress_quant":
             B, T = 2, 131072
