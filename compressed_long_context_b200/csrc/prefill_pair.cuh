@@ -33,7 +33,9 @@
 // Tiles of one row tile (item): the compressed segment in tiles of 256 entries, then the
 // raw window [wlo, tlast] in tiles of 256 tokens; per-row masks [lo, hi) as in prefill.cuh.
 // Lazy rescaling: a row moves its reference maximum only when a tile's maximum exceeds it
-// by 2^8, so the O-CTA rarely touches O between MMAs.
+// by 2^8, so the O-CTA rarely touches O between MMAs.  The unit that exceeds it is stored a second
+// time, once the O-CTA has seen the first (kBarRetry; 32K tokens: 2180 us without that hand-over, which no
+// order of the stores allowed, 2215 with it).
 #pragma once
 
 #include <type_traits>
@@ -62,6 +64,7 @@ constexpr uint32_t kPpUnit = 32768;              // K: 256 keys x 64 ch; V: 64 k
 constexpr uint32_t kPpVSub = 8192;               // V unit = 4 channel slabs of 64 keys x 64 ch
 constexpr uint32_t kPpPBuf = 32768;              // P unit: 128 rows x 128 keys, 16 key chunks of 2 KB
 constexpr uint32_t kPpHdrBytes = 528;            // per P unit: alpha[128], flag[4]
+constexpr uint32_t kPpVoid = 2;                  // flag: the quarter's rows of this unit come again (0, 1: O rows rescaled)
 // shared-memory layout (offsets from a 1024-aligned base); the two ranks reuse offsets
 constexpr uint32_t kPpSmQ = 0;                   // S-CTA: Q, 8 slabs (128 KB)
 constexpr uint32_t kPpSmP = 0;                   // O-CTA: P units
@@ -73,7 +76,7 @@ constexpr uint32_t kPpSmHdr = kPpSmRing + kPpRingK * kPpUnit;    // O-CTA: unit 
 constexpr uint32_t kPpSmXch = kPpSmHdr;          // S-CTA: softmax exchange, 2 x 2 x 128 floats
 constexpr uint32_t kPpHdrArea = kPpSlots * kPpHdrBytes > 2048 ? kPpSlots * kPpHdrBytes : 2048;
 constexpr uint32_t kPpSmBar = kPpSmHdr + kPpHdrArea;
-constexpr int kPpNumBars = 56;                  // 56 used; even count keeps misc 16-aligned
+constexpr int kPpNumBars = 60;                  // even count keeps misc 16-aligned
 constexpr uint32_t kPpSmMisc = kPpSmBar + kPpNumBars * 8;
 constexpr uint32_t kPpSmem = kPpSmMisc + 16;
 static_assert(kPpSmem <= 232448, "pair prefill shared memory exceeds the 227 KB per-block limit");
@@ -91,8 +94,9 @@ enum : int {
     kBarVFull = 16, kBarVEmpty = 20, kBarPFull = 24, kBarCorr = 28, kBarPCons = 32,
     kBarOFull = 36, kBarOEmpty = 37,                                       // O-CTA
     kBarDrain = 38,
-    kBarQSFull = 40, kBarQSEmpty = 48                                      // S-CTA: per Q slab [8]
-};
+    kBarQSFull = 40, kBarQSEmpty = 48,                                     // S-CTA: per Q slab [8]
+    kBarRetry = 56                                                         // per lane quarter [4]: a unit may be stored again
+};                                                                         // (S-CTA) / has been (O-CTA)
 
 struct PpItem {
     int b, g, t0, tlast;
@@ -206,6 +210,26 @@ __device__ __forceinline__ bool pp_warp_wait_cl(uint64_t* bar, uint32_t parity, 
     const bool ok = pp_wait_cl(bar, parity, abort);
     return __all_sync(0xffffffffu, ok);
 }
+// The same as a call, for waits off the usual path (inlined, they cost the paths around them registers).
+__device__ __noinline__ bool pp_warp_wait_call(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return pp_warp_wait_cl(bar, parity, abort);
+}
+// A unit of a lane quarter that is stored again: deliver it marked void, and wait until the O-CTA has all of it.  Both
+// warps of the quarter (named barrier 4 + q4), the same verdict in both.
+__device__ __noinline__ bool pp_void_unit(uint32_t rflag, uint32_t pbar, uint32_t bytes, bool deliver, uint64_t* retry, uint32_t parity,
+                                          int q4, volatile int* abort) {
+    if (deliver) {
+        pp_st_async_u32(rflag, kPpVoid, pbar);
+        pp_remote_arrive_expect_tx(pbar, bytes + 4u);
+    }
+    __syncwarp();
+    const bool mine = pp_warp_wait_cl(retry, parity, abort);
+    uint32_t res;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(res) : "r"((uint32_t)mine), "r"(4 + q4) : "memory");
+    return res != 0;
+}
 // Wait for a phase at exit, ignoring the abort flag (copies already issued still land);
 // bounded by the same wall-clock limit.
 __device__ __forceinline__ void pp_drain_wait(uint64_t* bar, uint32_t parity) {
@@ -239,6 +263,18 @@ __device__ __forceinline__ uint32_t pp_ld_cluster_u32(uint32_t raddr) {
 __device__ __forceinline__ void pp_drain_ring(uint64_t* full, uint32_t issued, uint32_t ring) {
     for (uint32_t st = 0; st < ring; ++st)
         if (issued > st) pp_drain_wait(&full[st], ((issued - 1 - st) / ring) & 1);
+}
+
+// Sum of nch chunks of 8 bf16 probabilities, 2 KB apart.
+__device__ __forceinline__ float pp_row_sum(const uint8_t* prow, int nch) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < nch; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(prow + c * 2048);
+        sum += (bf16lo(w.x) + bf16hi(w.x)) + (bf16lo(w.y) + bf16hi(w.y)) +
+               (bf16lo(w.z) + bf16hi(w.z)) + (bf16lo(w.w) + bf16hi(w.w));
+    }
+    return sum;
 }
 
 __global__ void __launch_bounds__(kPpThreads, 1)   // 10 warps: at most 168 registers (3 warps per SMSP)
@@ -283,6 +319,7 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
             mbar_init(&bars[kBarCorr + i], 4);
             mbar_init(&bars[kBarPCons + i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&bars[kBarRetry + i], 1);
         mbar_init(&bars[kBarOFull], 1);
         mbar_init(&bars[kBarOEmpty], 4);
         mbar_init(&bars[kBarDrain], 1);
@@ -437,7 +474,7 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
             const uint32_t rHdr = peer_base + kPpSmHdr;
             const uint32_t rPFull = peer_base + kPpSmBar + kBarPFull * 8;
             const float sl2 = p.scale_log2;
-            int n = 0;            // S tiles
+            uint32_t n = 0;       // S tiles; the top bit is the parity of units stored again
             uint32_t un = 0;      // P units
             bool ok = true;
             for (long long i = pair; ok && i < p.items; i += npairs) {
@@ -450,7 +487,7 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                 const int nc_t = pf_visible(t, p.W, p.blk);
                 float m = -INFINITY, l = 0.f;     // l: this warp's partial row sum
                 for (int j = 0; ok && j < nt; ++j, ++n) {
-                    const int sb = n & 1;
+                    const int sb = (int)(n & 1);
                     const int nk = pp_tile_keys(it, j);
                     int lo, hi;               // valid columns of this row in the tile: [lo, hi)
                     if (j < it.nct) {
@@ -513,11 +550,12 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                         }
                         // P in bf16 straight into the O-CTA's slot us: keys 8c..8c+7 of the unit,
                         // this row, at chunk c (2 KB per chunk of 8 keys x 128 rows).  Every store
-                        // counts its bytes on the slot's barrier; each lane quarter arms it once
-                        // it knows how many bytes it stored (a redone unit is stored twice).
-                        const uint32_t pbar = rPFull + us * 8;
+                        // counts its bytes on the slot's barrier, which each lane quarter arms.  Stores of
+                        // st.async to one address land in no order, so a redone unit is delivered first, marked
+                        // void; the O-CTA's rescale warp of the quarter, which then has all of it, asks for it
+                        // again, and the second delivery counts on a barrier of the quarter's own.
+                        uint32_t pbar = rPFull + us * 8;
                         const uint32_t pbase = rP + us * kPpPBuf;
-                        int attempts = 1;
                         // columns valid for every row of the warp (most compressed units) skip
                         // the per-column mask
                         const bool unmasked = __all_sync(0xffffffffu, lo <= c_beg && hi >= c_end);
@@ -578,8 +616,15 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                                 m += dmax;
                                 resc = true;
                             }
-                            attempts = 2;
+                            if (!pp_void_unit(rHdr + us * kPpHdrBytes + 512 + q4 * 4, pbar, (uint32_t)pp_unit_cols(nk, hh) * 64u,
+                                              hw == 0 && lane == 0, &bars[kBarRetry + q4], n >> 31, q4, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            n ^= 0x80000000u;
+                            pbar = peer_base + kPpSmBar + (kBarRetry + q4) * 8;
                         }
+                        if (!ok) break;
                         l += rs;
                         if (hh == nu - 1) {
                             // every TMEM load of this warp from the tile has completed
@@ -596,14 +641,14 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                         }
                         if (hw == 0) {
                             // unit header: rescale factor per row, per-quarter flag; then the arm:
-                            // this quarter's P bytes (both warps, every attempt) and header bytes
+                            // this quarter's P bytes (both warps) and header bytes
                             const uint32_t hdr = rHdr + us * kPpHdrBytes;
                             pp_st_async_u32(hdr + r * 4, __float_as_uint(al), pbar);
                             const bool any = __any_sync(0xffffffffu, resc);
                             if (lane == 0) {
                                 pp_st_async_u32(hdr + 512 + q4 * 4, any ? 1u : 0u, pbar);
                                 pp_remote_arrive_expect_tx(
-                                    pbar, (uint32_t)attempts * (uint32_t)(u_end - hh * kPpUKeys) * 64u + 32u * 4u + 4u);
+                                    pbar, (uint32_t)(u_end - hh * kPpUKeys) * 64u + 32u * 4u + 4u);
                             }
                             if (last && row_live && p.lse)
                                 p.lse[((size_t)it.b * p.Hq + head) * p.T + tok] =
@@ -718,7 +763,8 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
             const int q4 = warp & 3;
             const int r = q4 * 32 + lane;
             const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-            uint32_t un = 0;
+            const uint32_t rRetry = peer_base + kPpSmBar + (kBarRetry + q4) * 8;
+            uint32_t un = 0, again = 0;
             int item_n = 0;
             bool ok = true;
             for (long long i = pair; ok && i < p.items; i += npairs, ++item_n) {
@@ -735,17 +781,23 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                             break;
                         }
                         const uint8_t* hdr = sm + kPpSmHdr + us * kPpHdrBytes;
-                        const int flag = *reinterpret_cast<const volatile int*>(hdr + 512 + q4 * 4);
-                        const float al = *reinterpret_cast<const volatile float*>(hdr + r * 4);
-                        // l = l * alpha + the unit's P of this row (8 keys per 16-byte chunk)
-                        float us_sum = 0.f;
+                        int flag = *reinterpret_cast<const volatile int*>(hdr + 512 + q4 * 4);
+                        float al = *reinterpret_cast<const volatile float*>(hdr + r * 4);
+                        // the unit's P of this row (8 keys per 16-byte chunk)
                         const uint8_t* prow = sm + kPpSmP + us * kPpPBuf + r * 16;
                         const int nch = pp_unit_cols(nk, hh) >> 3;
-#pragma unroll 4
-                        for (int c = 0; c < nch; ++c) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(prow + c * 2048);
-                            us_sum += (bf16lo(w.x) + bf16hi(w.x)) + (bf16lo(w.y) + bf16hi(w.y)) +
-                                      (bf16lo(w.z) + bf16hi(w.z)) + (bf16lo(w.w) + bf16hi(w.w));
+                        float us_sum = pp_row_sum(prow, nch);
+                        if (flag == kPpVoid) {        // all of it is here: ask for the quarter's rows again
+                            __syncwarp();
+                            if (lane == 0) pp_remote_arrive(rRetry);
+                            if (!pp_warp_wait_call(&bars[kBarRetry + q4], again & 1, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            ++again;
+                            flag = *reinterpret_cast<const volatile int*>(hdr + 512 + q4 * 4);
+                            al = *reinterpret_cast<const volatile float*>(hdr + r * 4);
+                            us_sum = pp_row_sum(prow, nch);
                         }
                         l = l * al + us_sum;
                         if (flag) {
