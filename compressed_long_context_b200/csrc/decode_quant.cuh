@@ -37,10 +37,11 @@
 // What bounds it.  A small call: its chain of first steps, whose code is fetched cold (about 30 cycles an instruction).
 // So they are loops, not unrolled, the range is found by one warp, and the MMA issuers are elected: one 4K sequence
 // (one tile of each kind on two CTAs) takes 17.3 us with the merge, where unrolled set-up code and issuers chosen by
-// lane took 27.  A large one: the chain softmax - PV - reference of a tile (3 us, of which the MMAs take 1.6, bound by
-// the shared memory that they read: an M = 128, N = 64 MMA takes 48 cycles), and 8 us at each start of a unit.  256
-// sequences of 128K: 84 us and the merge, 4.7 TB/s of memory, every code read once, tensor pipe 24 % active.  Requesting
-// tiles into L2 ahead of the rings changed nothing at 1, 2 or 3 tiles.
+// lane took 27.  A large one: 3.0 us for each tile of codes from memory (6.5 TB/s while all SMs stream; 2.9 from L2, with QK
+// normalisation 3.7 and 3.3; the MMAs take 1.6 to 1.9, bound by the shared memory that they read: an M = 128, N = 64 MMA
+// takes 48 cycles), and 8 us at each start of a unit, which nothing hides.  256 sequences of 128K: 84 us and the merge, 4.7 TB/s
+// of memory over it all, every code read once, tensor pipe 24 % active.  Requesting tiles into L2 ahead of the rings changed
+// nothing at 1, 2 or 3 tiles.
 #pragma once
 
 #include "decode.cuh"
@@ -56,8 +57,9 @@ constexpr int kQdLook = 4;                 // S buffers at most
 // Tensor memory: S buffers (and K K^T) in columns 0 .. 255, O^T in 256 .. 511 (4 x 64 for 128 channels each).
 constexpr uint32_t kQdKK = 128, kQdO = 256;
 constexpr int kQdKept = 2048;              // units whose tile counts fit the P buffers while these are not in use
-// Cost of starting a unit, in tiles: query operand, refilled pipeline and record take about 8 us, a tile 4 us where all
-// SMs stream.  It lies before the unit's first tile, so a range that starts units holds fewer tiles.
+// Cost of starting a unit, in tiles: query operand, refilled pipeline and record take about 8 us, a tile 3.  It lies before
+// the unit's first tile, so a range that starts units holds fewer tiles.  128 sequences of 4K to 1M tokens with QK
+// normalisation, 256 and 160 of 128K: 159, 108 and 75.6 us; with a start of one tile 158, 110 and 75.3, of three 155, 108 and 79.
 constexpr int kQdStart = 2;
 constexpr float kQdShift = 4.0f;           // the reference m lies this far (log2) below the maximum
 
