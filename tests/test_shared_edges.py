@@ -182,3 +182,52 @@ def test_serving_on_a_shared_prefix(cuda_device, libhca, W, ps):
             moved = 2.0 ** -7 * torch.einsum("hn,hn->h", own, Q.abs() @ K[P:max(P, nc)].abs().T * 512 ** -0.5)[:, None] * 2 * mass
             for x in (got[b], ref[b]):
                 check(x, p @ V, mass * (2.0 ** -7 + 2 * d * 2.0 ** -18 + 2.0 ** -16) + step + 1.2 * moved, 2.0 ** -16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_lengths_change_between_replays(cuda_device, libhca, norm):
+    """A captured call follows the lengths on the device (both grids plan from them): short, long, mixed, padding rows."""
+    dev, B, Np = cuda_device, 9, 300
+    a = batch(dev, 6, B, 64, Np, 200, 40, [40] * B)
+    if norm:
+        a["gq"] = a["gk"] = torch.ones(512, device=dev)
+    lens = [[40] * B, [16 * 500 + 40] * B, [16 * (Np + 25 * i) + 41 + i for i in range(B)], [0, 3, 16 * 301 + 40, 0, 16 * 499 + 40, 39, 40, 5000, 1]]
+    want = []
+    for n in lens:
+        a["seqlens"].copy_(torch.tensor(n, dtype=torch.int32))
+        want.append(hca.decode_shared(**a))
+    done()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            got = hca.decode_shared(**a)
+        for n, w in list(zip(lens, want)) * 2:
+            a["seqlens"].copy_(torch.tensor(n, dtype=torch.int32))
+            gr.replay()
+            assert torch.equal(got, w)
+    done()
+
+
+@pytest.mark.gpu
+def test_shared_beside_other_work(cuda_device, libhca):
+    """Calls on three streams at once, one of them a prefill that fills the GPU: each has its own result."""
+    dev = cuda_device
+    a = [batch(dev, s, 6, 64, 500, 30, 40, [16 * (500 + 4 * i) + 50 for i in range(6)]) for s in range(2)]
+    a[1]["gq"] = a[1]["gk"] = torch.ones(512, device=dev)
+    g = torch.Generator(device=dev).manual_seed(9)
+    q, k, v = (torch.randn(1, 2000, h, 512, generator=g, device=dev).to(bf) for h in (64, 1, 1))
+    kc, vc = hca.compress(k, v, blk=16)
+    calls = [lambda: hca.decode_shared(**a[0]), lambda: hca.decode_shared(**a[1]), lambda: hca.prefill(q, k, v, kc, vc, 16, 128, 512 ** -0.5)]
+    want = [f() for f in calls]
+    done()
+    streams, got = [torch.cuda.Stream() for _ in calls], [[], [], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(calls[i]())
+    done()
+    for w, x in zip(want, got):
+        assert all(torch.equal(y, w) for y in x)
