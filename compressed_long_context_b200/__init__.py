@@ -429,6 +429,16 @@ def _scale_type(sc):
     return dtype
 
 
+def _wrong(e, *specs):
+    """The error for the first of these (tensor, dimensions, name) that is not a tensor of so many dimensions, else e."""
+    for t, dim, name in specs:
+        if not isinstance(t, torch.Tensor):
+            return TypeError("%s must be a torch.Tensor" % name)
+        if t.dim() != dim:
+            return ValueError("%s must have %d dimensions, got %d" % (name, dim, t.dim()))
+    return e
+
+
 def _run(name, dev, *args):
     """One call of the library on the tensors' device and its current stream."""
     fn = getattr(_lib.load(), name)
@@ -458,7 +468,10 @@ def _cache_shape(kc, page_table, B, device):
     if page_table is None:
         n = kc.shape[1]
         return 0, 0, 0, 0, n, B * n
-    max_pages = page_table.shape[1]
+    try:
+        max_pages = page_table.shape[1]
+    except (AttributeError, IndexError) as e:
+        raise _wrong(e, (page_table, 2, "page_table")) from None
     _all(device, (page_table, _I32, B * max_pages, "page_table"))
     pages, size = kc.shape[:2]
     return HCA_PAGED, size, max_pages, pages, 0, pages * size
@@ -470,8 +483,11 @@ def compress_quant(k, v, w=None, blk=128, kc=None, vc=None, sc=None):
     [B, T // blk, Hkv, 2] (key, value); an entry's value is code * scale."""
     _need(k, _BF16, "k")
     dev = k.device
-    B, T, Hkv, d = k.shape
-    dv = v.shape[3]
+    try:
+        B, T, Hkv, d = k.shape
+        dv = v.shape[3]
+    except (AttributeError, IndexError, ValueError) as e:
+        raise _wrong(e, (k, 4, "k"), (v, 4, "v")) from None
     Nc = T // blk if blk > 0 else 0
     n = B * Nc * Hkv
     if kc is None:
@@ -494,9 +510,12 @@ def append_quant(k_new, v_new, w_new, seqlens, kw, vw, kc, vc, sc, state, blk, p
     page_table) and sc (its scales).  Other arguments as for ``append``; seqlens[b] == 0 skips a row."""
     _need(k_new, _BF16, "k_new")
     dev = k_new.device
-    B, Hkv, d = k_new.shape
-    dv, W = v_new.shape[2], kw.shape[1]
-    flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
+    try:
+        B, Hkv, d = k_new.shape
+        dv, W = v_new.shape[2], kw.shape[1]
+        flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
+    except (AttributeError, IndexError, ValueError) as e:
+        raise _wrong(e, (k_new, 3, "k_new"), (v_new, 3, "v_new"), (kw, 4, "kw"), (kc, 4, "kc")) from None
     dtype = getattr(state, "dtype", None)
     if dtype is not _U8 and dtype is not _F32:
         raise TypeError("state must be a uint8 or float32 torch.Tensor")
@@ -522,7 +541,10 @@ def read_quant(kc, vc, sc, counts, n, page_table=None, k_out=None, v_out=None):
     are (zero in tensors that this call makes)."""
     _need(kc, _E4M3, "kc")
     dev = kc.device
-    B, Hkv, d, dv = counts.shape[0], kc.shape[2], kc.shape[3], vc.shape[3]
+    try:
+        B, Hkv, d, dv = counts.shape[0], kc.shape[2], kc.shape[3], vc.shape[3]
+    except (AttributeError, IndexError) as e:
+        raise _wrong(e, (counts, 1, "counts"), (kc, 4, "kc"), (vc, 4, "vc")) from None
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
     if k_out is None:
         k_out = torch.zeros((B, n, Hkv, d), dtype=_BF16, device=dev)
@@ -539,7 +561,7 @@ def read_quant(kc, vc, sc, counts, n, page_table=None, k_out=None, v_out=None):
 def _decode_options(dev, B, Hq, d, dv, W, kw, vw, gq, gk, gate, out, window_ring, vha_u, vha_v, out_f32, q):
     """(flags, out, rank) of the arguments that decode_quant and decode_shared have in common."""
     flags = 0
-    if kw.shape[1] != W or vw.shape[1] != W:
+    if kw.dim() != 4 or vw.dim() != 4 or kw.shape[1] != W or vw.shape[1] != W:
         raise ValueError("kw and vw must be [B, W, Hkv, 512] with W = %d" % W)
     if gq is not None or gk is not None:
         _all(dev, (gq, _F32, d, "gq"), (gk, _F32, d, "gk"))
@@ -573,8 +595,11 @@ def decode_quant(q, kc, vc, sc, kw, vw, seqlens, blk, W, scale, page_table=None,
     Returns out [B,Hq,512] bf16 (fp32 with out_f32); a row with seqlens[b] == 0 is zero."""
     _need(q, _BF16, "q")
     dev = q.device
-    B, Hq, d = q.shape
-    Hkv, dv = kc.shape[2], vc.shape[3]
+    try:
+        B, Hq, d = q.shape
+        Hkv, dv = kc.shape[2], vc.shape[3]
+    except (AttributeError, IndexError, ValueError) as e:
+        raise _wrong(e, (q, 3, "q"), (kc, 4, "kc"), (vc, 4, "vc")) from None
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
     n = rows * Hkv
     _all(dev, (kc, _E4M3, n * d, "kc"), (vc, _E4M3, n * dv, "vc"), (sc, _scale_type(sc), 2 * n, "sc"),
@@ -604,8 +629,14 @@ def decode_shared(q, kp, vp, kc, vc, kw, vw, seqlens, blk, W, scale, page_table=
     (window_ring=True) begins with the prefix's last W tokens, position p in slot (p - Np * blk) % W; Np * blk >= W."""
     _need(q, _BF16, "q")
     dev = q.device
-    B, Hq, d = q.shape
-    Np, Hkv, dv = kp.shape[0], kc.shape[2], vc.shape[3]
+    try:
+        B, Hq, d = q.shape
+        Hkv, dv = kc.shape[2], vc.shape[3]
+        Np, Hp, dp = kp.shape              # (a batch's entries have one dimension more: kp = kc[0])
+        if Hp != Hkv or dp != d or vp.shape != (Np, Hkv, dv):
+            raise ValueError("kp and vp must be [Np, %d, 512], got %s and %s" % (Hkv, tuple(kp.shape), tuple(vp.shape)))
+    except (AttributeError, IndexError, ValueError) as e:
+        raise _wrong(e, (q, 3, "q"), (kp, 3, "kp"), (vp, 3, "vp"), (kc, 4, "kc"), (vc, 4, "vc")) from None
     flags, page_size, max_pages, num_pages, Nmax, rows = _cache_shape(kc, page_table, B, dev)
     n = rows * Hkv
     _all(dev, (kp, _BF16, Np * Hkv * d, "kp"), (vp, _BF16, Np * Hkv * dv, "vp"), (kc, _BF16, n * d, "kc"),

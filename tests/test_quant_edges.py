@@ -5,7 +5,8 @@ import torch
 
 import compressed_long_context_b200 as hca
 from compressed_long_context_b200 import _lib
-from test_quant import check, decode_case, done
+from test_binding_host import stub  # noqa: F401
+from test_quant import check, decode_case, done, z
 from test_shared import make
 
 bf, f8, e8 = torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu
@@ -281,3 +282,38 @@ def test_norm_prefix_is_held_in_eleven_bits(cuda_device, libhca):
     for b, (_, _, p, two, _) in enumerate(rows):
         rel = shared_norm_check(got[b, :, :400].double(), p, two)
         assert rel <= 1, rel
+
+
+def test_arguments_of_the_wrong_kind(stub):  # noqa: F811
+    """What is not a tensor is a TypeError and a wrong number of dimensions a ValueError, before anything reaches the library; a
+    prefix that still has its batch dimension would have been read as one entry."""
+    B, W, i32 = 2, 9, torch.int32
+    cache = dict(kc=z(B, 7, 1, 512, dtype=f8), vc=z(B, 7, 1, 512, dtype=f8), sc=z(B, 7, 1, 2, dtype=e8))
+    window = dict(kw=z(B, W, 1, 512), vw=z(B, W, 1, 512), seqlens=z(B, dtype=i32))
+    step = dict(q=z(B, 64, 512), blk=16, W=W, scale=0.1, workspace=z(64, dtype=torch.uint8), **window)
+    own = dict(kc=z(B, 7, 1, 512), vc=z(B, 7, 1, 512))
+    calls = {
+        "compress_quant": (dict(k=z(B, 32, 1, 64), v=z(B, 32, 1, 64), blk=16), [("k", z(B, 32, 64)), ("v", z(B, 32, 64))]),
+        "append_quant": (dict(k_new=z(B, 1, 512), v_new=z(B, 1, 512), w_new=None, state=torch.zeros(1028 * B), blk=16, **cache, **window),
+                         [("k_new", z(B, 512)), ("v_new", z(512)), ("kw", z(9)), ("kc", z(9, dtype=f8)), ("page_table", z(4, dtype=i32))]),
+        "read_quant": (dict(counts=z(B, dtype=i32), n=3, **cache), [("kc", z(7, 512, dtype=f8)), ("vc", z(7, dtype=f8)),
+                                                                    ("page_table", z(4, dtype=i32))]),
+        "decode_quant": (dict(**step, **cache), [("q", z(B, 512)), ("kc", z(7, 512, dtype=f8)), ("vc", z(7, 512, dtype=f8)),
+                                                 ("kw", z(B * W * 512)), ("page_table", z(4, dtype=i32))]),
+        "decode_shared": (dict(kp=z(5, 1, 512), vp=z(5, 1, 512), **step, **own),
+                          [("q", z(B, 512)), ("kp", z(1, 5, 1, 512)), ("vp", z(1, 5, 1, 512)), ("kp", z(5, 512)), ("kc", z(7, 512)),
+                           ("vw", z(B * W * 512)), ("page_table", z(4, dtype=i32))]),
+    }
+    for name, (good, bad) in calls.items():
+        call = getattr(hca, name)
+        call(**good)
+        n = len(stub.calls)
+        for arg, t in bad:
+            with pytest.raises(ValueError):
+                call(**{**good, arg: t})
+            with pytest.raises(TypeError):
+                call(**{**good, arg: t.tolist() if t.dtype in (bf, i32) else "codes"})
+        assert len(stub.calls) == n
+    a = {**calls["decode_shared"][0], "kp": z(1, 5, 1, 512), "vp": z(1, 5, 1, 512)}      # both with the batch dimension
+    with pytest.raises(ValueError, match="kp"):
+        hca.decode_shared(**a)
