@@ -9,7 +9,7 @@ bf = torch.bfloat16
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("step,rise", [(1, 12.0), (2, 20.0), (3, 40.0)])
+@pytest.mark.parametrize("step,rise", [(1, 12.0), (1, 36.0), (2, 20.0), (3, 40.0)])
 def test_references_move(cuda_device, libhca, step, rise):
     """Half of the heads' logits rise by 2^rise every `step` units of entries, the other half's fall.  A unit that moves a
     reference is followed by units that weigh as much, so probabilities against an older reference would show; and the same
