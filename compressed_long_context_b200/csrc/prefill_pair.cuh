@@ -33,9 +33,11 @@
 // Tiles of one row tile (item): the compressed segment in tiles of 256 entries, then the
 // raw window [wlo, tlast] in tiles of 256 tokens; per-row masks [lo, hi) as in prefill.cuh.
 // Lazy rescaling: a row moves its reference maximum only when a unit's maximum exceeds it
-// by 2^32, so the O-CTA rarely touches O between MMAs.  The unit that exceeds it is stored a second
-// time, once the O-CTA has seen the first (kBarRetry; the code for it costs 1.6 %: 128K tokens 15.36 ms, against
-// 15.11 without the hand-over, which no order of the stores allowed).
+// by 2^8, so the O-CTA rarely touches O between MMAs.  The unit that exceeds it is stored a second
+// time, once the O-CTA has seen the first (kBarRetry); the window's units, where single tokens stand out among
+// means, take their maximum before they are stored.  128K tokens, one raw key in a hundred 8 times larger: 15.15 ms, 16.34 without
+// the window's maxima, 15.36 with references that move at 2^32 instead (and errors a tenth larger, since a row's largest P is then
+// seldom exactly 1); no key standing out: 14.7, 14.55 and 14.55 ms.
 #pragma once
 
 #include <type_traits>
@@ -86,11 +88,6 @@ static_assert(kPpKeys == 2 * kPpUKeys, "an S tile is two P units");
 static_assert(kPpSlots <= 4 && kPpRingV <= 4 && kPpRingK == 3, "barrier index ranges");
 static_assert(kPpSmVRing + kPpRingV * kPpUnit <= kPpSmHdr, "O-CTA: P, staging and the V ring fit");
 static_assert(kPpSmVRing % 1024 == 0, "V units 1024-aligned");
-
-// A row's reference moves when a logit exceeds it by this (log2).  P = 2^(z - m) is a floating number, so its relative
-// precision does not depend on m; the bound only keeps sums of P v in range (|v| < 2^80).  A move delivers a unit twice: 128K
-// tokens, one raw key in a hundred 8 times larger, 16.34 ms with 2^8 and 15.36 with 2^32.
-constexpr float kPpRescale = 32.f;
 
 // barrier indices (both ranks initialise all of them; each rank uses its own)
 enum : int {
@@ -517,9 +514,10 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                         const int c_end = min(c_beg + 64, u_end);             // (may be empty)
                         // The reference maximum m of a row is lazy: P = 2^(logit - m) is computed
                         // against the reference of the earlier units, and m moves only when a unit
-                        // exceeds it by kPpRescale -- the unit is then redone against the new reference.
-                        // A quarter in which some row has no reference yet takes the maximum first.
-                        const bool need_max = __any_sync(0xffffffffu, m == -INFINITY);
+                        // exceeds it by kPfRescale -- the unit is then redone against the new reference.
+                        // A quarter in which some row has no reference yet takes the maximum first, and so
+                        // does every unit of the window.
+                        const bool need_max = j >= it.nct || __any_sync(0xffffffffu, m == -INFINITY);
                         bool resc = false;
                         float al = 1.f;
                         if (need_max) {
@@ -540,7 +538,7 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                             float tother;
                             exchange(tmax, &tother);
                             tmax = fmaxf(tmax, tother);
-                            resc = m != -INFINITY && tmax > m + kPpRescale;
+                            resc = m != -INFINITY && tmax > m + kPfRescale;
                             if (resc) {
                                 al = ex2(m - tmax);
                                 l *= al;
@@ -613,7 +611,7 @@ prefill_pair_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap t
                             float dother;
                             exchange(dmax, &dother);
                             dmax = fmaxf(dmax, dother);
-                            const bool over = dmax > kPpRescale;
+                            const bool over = dmax > kPfRescale;
                             if (!__any_sync(0xffffffffu, over)) break;
                             if (over) {
                                 al = ex2(-dmax);
